@@ -136,6 +136,28 @@ _SIGNATURES.update({
     "bitlinear_chain_run_timeout_test": (_int, [_vp, _int, ctypes.c_uint64, _vp]),
 })
 
+class HeadsC(ctypes.Structure):
+    """Mirror of bitlinear_heads (include/bitlinear.h)."""
+    _fields_ = [("data", ctypes.c_void_p),
+                ("rows", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+_heads_p = ctypes.POINTER(HeadsC)
+_SIGNATURES.update({
+    "bitlinear_qk_norm_rope": (_int, [_heads_p, _heads_p, _heads_p, _int, _int, _int, _int, _vp,
+                                      _vp, _i64, _vp, _vp, _int, ctypes.c_float, _vp, _heads_p,
+                                      _heads_p, _heads_p, ctypes.c_uint, _vp]),
+    "bitlinear_attention_prefill_workspace_bytes": (_sz, [_int, _int]),
+    "bitlinear_attention_prefill": (_int, [_heads_p, _heads_p, _heads_p, _vp, _vp, _int, _int, _int,
+                                           _int, ctypes.c_float, _heads_p, _vp, _sz, ctypes.c_uint,
+                                           _vp]),
+    "bitlinear_adapter_workspace_bytes": (_sz, [_i64, _int]),
+    "bitlinear_adapter_add": (_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _int,
+                                     _int, _vp, _vp, _vp, _i64, _vp, _sz, ctypes.c_uint, _vp]),
+})
+
 for _name, (_res, _args) in _SIGNATURES.items():
     _fn = getattr(_lib, _name)
     _fn.restype = _res
@@ -630,6 +652,198 @@ def position_advance(pos: torch.Tensor):
     with _on(pos.device):
         _check(_lib.bitlinear_position_advance(_ptr(pos), _stream(pos.device)),
                "bitlinear_position_advance")
+
+
+BL_FLAG_ROPE_HALVES = 8
+
+
+def _heads(t, where: str, name: str, dtypes, heads: int | None = None, rows: int | None = None):
+    """The rows of heads [rows][heads][128] of a tensor, any strides above the
+    contiguous 128 values of a head."""
+    if t.dtype not in dtypes:
+        want = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise BitLinearError(BL_ERR_DTYPE, where,
+                             f"{name} is {str(t.dtype).replace('torch.', '')}, needs {want}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 128 or t.stride(2) != 1 or shape[0] < 1 or shape[1] < 1 or \
+            (heads is not None and shape[1] != heads) or (rows is not None and shape[0] != rows):
+        raise BitLinearError(
+            BL_ERR_SHAPE, where, f"{name} of shape {tuple(shape)} and strides {tuple(t.stride())} is not "
+            f"[{'rows' if rows is None else rows}][{'heads' if heads is None else heads}][128]")
+    return HeadsC(t.data_ptr(), shape[0], t.stride(0), t.stride(1))
+
+
+def _vector(t, where: str, name: str, dtypes, n: int):
+    """A contiguous vector (or array) of at least n elements."""
+    if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < n:
+        _fits(t, where, name, dtypes, 1, n)
+
+
+def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float = RMS_EPS,
+                 slots=None, q_out=None, k_out=None, v_out=None, halves: bool = False,
+                 pdl: bool = False):
+    """Queries and keys of T tokens in one pass: RMS norm of each head (with
+    q_gain / k_gain [128]; none without), rotation by the token's position, keys
+    and values written to their cache rows.  Returns (q_out, k_out, v_out).
+
+    q [T, H, 128], k and v [T, Hkv, 128]: fp32 or bf16, any row and head
+    strides (parts of one fused projection, for example); v may be None.
+    positions: int32 [T], rows of `table` (rope_table).  slots: int32 [T], the
+    row of k_out / v_out [rows, Hkv, 128] of each token (a cache
+    [Hkv, T_max, 128] is passed as cache.transpose(0, 1)), negative for padding
+    whose key and value are written nowhere; without slots token t has row t.
+    Non-negative slots must differ from one another.  halves: the rotated pairs
+    of a head are (i, i + 64) instead of (2i, 2i + 1).  Outputs are bf16; one
+    may be its own input, in place.
+    """
+    where = "bitlinear_qk_norm_rope"
+    if q.dim() != 3 or k.dim() != 3:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"q of shape {tuple(q.shape)}, k of shape {tuple(k.shape)}")
+    T, H, Hkv = q.shape[0], q.shape[1], k.shape[1]
+    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+        raise BitLinearError(BL_ERR_DTYPE, where, "q, k and v of mixed element types")
+    if (v is None and v_out is not None) or (slots is not None and (
+            k_out is None or (v is not None and v_out is None))):
+        raise BitLinearError(BL_ERR_NULL, where, "slots need k_out and v_out, v_out needs v")
+    if q_out is None:
+        q_out = torch.empty(T, H, 128, dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=q.device)
+    if v is not None and v_out is None:
+        v_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=q.device)
+    qh, kh = _heads(q, where, "q", _FLOATS), _heads(k, where, "k", _FLOATS, Hkv, T)
+    vh = None if v is None else _heads(v, where, "v", _FLOATS, Hkv, T)
+    qo, ko = _heads(q_out, where, "q_out", _BF16, H, T), _heads(k_out, where, "k_out", _BF16, Hkv)
+    vo = None if v is None else _heads(v_out, where, "v_out", _BF16, Hkv, ko.rows)
+    if slots is None and ko.rows < T:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"k_out has {ko.rows} rows for {T} tokens")
+    _vector(positions, where, "positions", _I32, T)
+    if table.dim() != 3 or table.shape[1] != 64 or table.shape[2] != 2:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"table of shape {tuple(table.shape)} is not [positions][64][2]")
+    _vector(table, where, "table", _F32, table.shape[0] * 128)
+    gt = BL_F32
+    for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if g is not None:
+            _vector(g, where, name, _FLOATS, 128)
+            gt = _dt(g.dtype)
+    if q_gain is not None and k_gain is not None and q_gain.dtype != k_gain.dtype:
+        raise BitLinearError(BL_ERR_DTYPE, where, "gains of mixed element types")
+    if slots is not None:
+        _vector(slots, where, "slots", _I32, T)
+    flags = (BL_FLAG_PDL if pdl else 0) | (BL_FLAG_ROPE_HALVES if halves else 0)
+    with _on(q.device):
+        _check(_lib.bitlinear_qk_norm_rope(qh, kh, vh, _dt(q.dtype), H, Hkv, 128, _ptr(positions),
+                                           _ptr(table), table.shape[0], _ptr(q_gain), _ptr(k_gain), gt,
+                                           float(eps), _ptr(slots), qo, ko, vo, flags,
+                                           _stream(q.device)), where)
+    return q_out, k_out, v_out
+
+
+def attention_prefill_workspace(H: int, Hkv: int, device) -> torch.Tensor:
+    """A workspace for attention_prefill of any lengths (reusable by ordered
+    calls; its contents do not matter)."""
+    dev = torch.device(device)
+    with _on(dev):
+        n = int(_lib.bitlinear_attention_prefill_workspace_bytes(H, Hkv))
+    if n == 0:
+        raise BitLinearError(BL_ERR_SHAPE, "bitlinear_attention_prefill_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=None,
+                      workspace=None, pdl: bool = False):
+    """Causal attention of packed sequences with grouped heads.
+
+    q [Tq, H, 128], k and v [Tk, Hkv, 128], bf16, any row and head strides (a
+    cache [Hkv, T_max, 128] is passed as cache.transpose(0, 1)).  Sequence b has
+    the query rows cu_q[b] .. cu_q[b + 1] - 1 and the key rows cu_k[b] ..
+    cu_k[b + 1] - 1 (int32 [sequences + 1] on the GPU; cu_k is cu_q unless
+    given); its queries are its last positions: with nq queries and nk keys,
+    query i sees the keys 0 .. i + nk - nq, and gets zeros if there are none.
+    So cu_q = cu_k is a batch of whole prompts, nk > nq a piece of a prompt
+    behind a cached past, nq = 1 one new token for each request.  Rows of `out`
+    outside every sequence stay as they were.
+    """
+    where = "bitlinear_attention_prefill"
+    if q.dim() != 3 or k.dim() != 3:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"q of shape {tuple(q.shape)}, k of shape {tuple(k.shape)}")
+    if cu_k is None:
+        cu_k = cu_q
+    if out is None:
+        out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+    T, H, Hkv = q.shape[0], q.shape[1], k.shape[1]
+    if Hkv < 1 or H % Hkv:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"{H} query heads for {Hkv} kv heads")
+    qh, kh = _heads(q, where, "q", _BF16), _heads(k, where, "k", _BF16)
+    vh, oh = _heads(v, where, "v", _BF16, Hkv, kh.rows), _heads(out, where, "out", _BF16, H, T)
+    batch = cu_q.numel() - 1
+    _vector(cu_q, where, "cu_q", _I32, 2)
+    _vector(cu_k, where, "cu_k", _I32, 2)
+    if cu_k.numel() != batch + 1:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"cu_q of {batch + 1} bounds, cu_k of {cu_k.numel()}")
+    if workspace is None:
+        workspace = attention_prefill_workspace(H, Hkv, q.device)
+    _vector(workspace, where, "workspace", (workspace.dtype,), 1)
+    with _on(q.device):
+        _check(_lib.bitlinear_attention_prefill(
+            qh, kh, vh, _ptr(cu_q), _ptr(cu_k), batch, H, Hkv, 128,
+            128 ** -0.5 if scale is None else float(scale), oh, _ptr(workspace),
+            workspace.numel() * workspace.element_size(), BL_FLAG_PDL if pdl else 0,
+            _stream(q.device)), where)
+    return out
+
+
+def adapter_workspace(T: int, r: int, device) -> torch.Tensor:
+    """A workspace for adapter_add of up to T tokens and rank r (reusable by
+    ordered calls; its contents do not matter)."""
+    dev = torch.device(device)
+    with _on(dev):
+        n = int(_lib.bitlinear_adapter_workspace_bytes(T, r))
+    if n == 0:
+        raise BitLinearError(BL_ERR_SHAPE, "bitlinear_adapter_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def adapter_add(y, x, down, up, index, scale=None, out=None, workspace=None, pdl: bool = False):
+    """Low-rank adapters of many requests beside one shared projection:
+    out[t] = y[t] + scale[a] * up[a] @ (down[a] @ x[t]) with a = index[t], and
+    out[t] = y[t] where index[t] is negative.
+
+    y [T, N] fp32 or bf16: the projection's output (linear, gemm); x [T, K]
+    bf16: its input; down [n, r, K] and up [n, N, r] bf16: n adapters, ranks
+    filled up with zeros to a common r (a multiple of 8 up to 128); index int32
+    [T] (tokens in any order); scale fp32 [n] or None (1).  out may be y itself
+    (the default is a new tensor).
+    """
+    where = "bitlinear_adapter_add"
+    if y.dim() != 2 or x.dim() != 2 or down.dim() != 3 or up.dim() != 3:
+        raise BitLinearError(BL_ERR_SHAPE, where, "y and x have two dimensions, down and up three")
+    (T, N), K, (n, r) = y.shape, x.shape[1], down.shape[:2]
+    if tuple(down.shape) != (n, r, K) or tuple(up.shape) != (n, N, r):
+        raise BitLinearError(BL_ERR_SHAPE, where, f"down of shape {tuple(down.shape)} and up of shape "
+                             f"{tuple(up.shape)} for K={K}, N={N}")
+    if out is None:
+        out = torch.empty(T, N, dtype=y.dtype, device=y.device)
+    if out.dtype != y.dtype:
+        raise BitLinearError(BL_ERR_DTYPE, where, "out and y of different element types")
+    ldy, ldx, ldo = (t.stride(0) if T > 1 else t.shape[1] for t in (y, x, out))
+    _fits(y, where, "y", _FLOATS, T, N, ldy)
+    _fits(x, where, "x", _BF16, T, K, ldx)
+    _fits(out, where, "out", _FLOATS, T, N, ldo)
+    _vector(down, where, "down", _BF16, n * r * K)
+    _vector(up, where, "up", _BF16, n * N * r)
+    _vector(index, where, "index", _I32, T)
+    if scale is not None:
+        _vector(scale, where, "scale", _F32, n)
+    if workspace is None:
+        workspace = adapter_workspace(T, r, y.device)
+    _vector(workspace, where, "workspace", (workspace.dtype,), 1)
+    with _on(y.device):
+        _check(_lib.bitlinear_adapter_add(
+            _ptr(y), _dt(y.dtype), ldy, _ptr(x), ldx, T, N, K, _ptr(down), _ptr(up), n, r, _ptr(index),
+            _ptr(scale), _ptr(out), ldo, _ptr(workspace), workspace.numel() * workspace.element_size(),
+            BL_FLAG_PDL if pdl else 0, _stream(y.device)), where)
+    return out
 
 
 @dataclass

@@ -627,6 +627,186 @@ int bitlinear_position_advance(int32_t *pos, void *stream)
     return launch_position_advance(pos, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+constexpr int64_t kMaxHeadsStride = int64_t(1) << 38;
+
+// Rows of heads: at least one row; strides that are read (sizes above one)
+// at least a head long and in range.
+bool valid_heads(const bitlinear_heads &h, int heads)
+{
+    auto ok = [](int64_t n, int64_t stride) { return n == 1 || (stride >= 128 && stride < kMaxHeadsStride); };
+    return h.rows >= 1 && h.rows < (int64_t(1) << 31) && ok(h.rows, h.row_stride) && ok(heads, h.head_stride);
+}
+
+// No two heads of the rows share memory: rows nested in heads or heads in rows.
+bool distinct_heads(const bitlinear_heads &h, int heads)
+{
+    const int64_t across = (heads == 1 ? 0 : (heads - 1) * h.head_stride) + 128;
+    if (h.rows == 1)
+        return true;
+    if (h.row_stride >= across)
+        return true;
+    return heads == 1 || (h.head_stride - 128) / h.row_stride >= h.rows - 1;
+}
+
+bool aligned_heads(const bitlinear_heads &h, int heads, int esz)
+{
+    return aligned16(h.data) && (h.rows == 1 || h.row_stride * esz % 16 == 0) &&
+           (heads == 1 || h.head_stride * esz % 16 == 0);
+}
+
+}  // namespace
+
+int bitlinear_qk_norm_rope(const bitlinear_heads *q, const bitlinear_heads *k, const bitlinear_heads *v,
+                           int xt, int H, int Hkv, int D, const int32_t *positions,
+                           const float *table, int64_t table_rows, const void *q_gain,
+                           const void *k_gain, int gt, float eps, const int32_t *slots,
+                           const bitlinear_heads *q_out, const bitlinear_heads *k_out,
+                           const bitlinear_heads *v_out, unsigned flags, void *stream)
+{
+    if (!q || !k || !q_out || !k_out || !positions || !table || !q->data || !k->data || !q_out->data ||
+        !k_out->data)
+        return BL_ERR_NULL;
+    const bool has_v = v && v->data;
+    if (has_v != (v_out && v_out->data))
+        return BL_ERR_NULL;
+    if (!valid_dtype(xt) || ((q_gain || k_gain) && !valid_dtype(gt)))
+        return BL_ERR_DTYPE;
+    if (D != 128 || H < 1 || Hkv < 1 || H > 1024 || Hkv > 1024 || table_rows < 1 ||
+        table_rows > (int64_t(1) << 31) || (flags & ~(BL_FLAG_PDL | BL_FLAG_ROPE_HALVES)) ||
+        ((q_gain || k_gain) && (!(eps >= 0.0f) || !(eps <= 3.0e38f))))
+        return BL_ERR_SHAPE;
+    const int64_t T = q->rows;
+    if (!valid_heads(*q, H) || !valid_heads(*k, Hkv) || !valid_heads(*q_out, H) || !valid_heads(*k_out, Hkv) ||
+        k->rows != T || q_out->rows != T || (!slots && k_out->rows < T) || !distinct_heads(*q_out, H) ||
+        !distinct_heads(*k_out, Hkv))
+        return BL_ERR_SHAPE;
+    if (has_v && (!valid_heads(*v, Hkv) || v->rows != T || !valid_heads(*v_out, Hkv) ||
+                  v_out->rows != k_out->rows || !distinct_heads(*v_out, Hkv)))
+        return BL_ERR_SHAPE;
+    const int esz = elem_bytes(xt);
+    if (!aligned_heads(*q, H, esz) || !aligned_heads(*k, Hkv, esz) || !aligned_heads(*q_out, H, 2) ||
+        !aligned_heads(*k_out, Hkv, 2) || !aligned16(q_gain) || !aligned16(k_gain) ||
+        (has_v && (!aligned_heads(*v, Hkv, esz) || !aligned_heads(*v_out, Hkv, 2))) ||
+        (reinterpret_cast<uintptr_t>(table) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+        (reinterpret_cast<uintptr_t>(slots) & 3u))
+        return BL_ERR_ALIGN;
+    const DeviceInfo *di;
+    int st = need_device(&di);
+    if (st)
+        return st;
+    if ((st = check_dev_ptrs({q->data, k->data, has_v ? v->data : nullptr, positions, table, q_gain, k_gain, slots,
+                              q_out->data, k_out->data, has_v ? v_out->data : nullptr})))
+        return st;
+    QkNormRopeArgs a{};
+    a.q = *q;
+    a.k = *k;
+    a.q_out = *q_out;
+    a.k_out = *k_out;
+    if (has_v) {
+        a.v = *v;
+        a.v_out = *v_out;
+    }
+    a.xt = xt;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.positions = positions;
+    a.table = table;
+    a.table_rows = table_rows;
+    a.q_gain = q_gain;
+    a.k_gain = k_gain;
+    a.gt = gt;
+    a.eps = eps;
+    a.slots = slots;
+    a.flags = flags;
+    return launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+bool valid_groups(int H, int Hkv)
+{
+    return H >= 1 && Hkv >= 1 && H <= 1024 && H % Hkv == 0 && H / Hkv <= kPrefillMaxGroup;
+}
+
+}  // namespace
+
+size_t bitlinear_attention_prefill_workspace_bytes(int H, int Hkv)
+{
+    if (!valid_groups(H, Hkv))
+        return 0;
+    return attention_prefill_workspace_bytes(H, Hkv);
+}
+
+int bitlinear_attention_prefill(const bitlinear_heads *q, const bitlinear_heads *k,
+                                const bitlinear_heads *v, const int32_t *cu_q,
+                                const int32_t *cu_k, int batch, int H, int Hkv, int D,
+                                float scale, const bitlinear_heads *out, void *ws,
+                                size_t ws_bytes, unsigned flags, void *stream)
+{
+    if (!q || !k || !v || !out || !cu_q || !cu_k || !q->data || !k->data || !v->data || !out->data)
+        return BL_ERR_NULL;
+    if (D != 128 || !valid_groups(H, Hkv) || batch < 1 || batch > 65535 || !(scale > 0.0f) ||
+        !(scale <= 3.0e38f) || (flags & ~BL_FLAG_PDL) || !valid_heads(*q, H) || !valid_heads(*k, Hkv) ||
+        !valid_heads(*v, Hkv) || !valid_heads(*out, H) || v->rows != k->rows || out->rows != q->rows ||
+        !distinct_heads(*out, H))
+        return BL_ERR_SHAPE;
+    if (!aligned_heads(*q, H, 2) || !aligned_heads(*k, Hkv, 2) || !aligned_heads(*v, Hkv, 2) ||
+        !aligned_heads(*out, H, 2) || !aligned16(ws) || (reinterpret_cast<uintptr_t>(cu_q) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cu_k) & 3u))
+        return BL_ERR_ALIGN;
+    const DeviceInfo *di;
+    int st = need_device(&di);
+    if (st)
+        return st;
+    if ((st = check_dev_ptrs({q->data, k->data, v->data, cu_q, cu_k, out->data, ws})))
+        return st;
+    if (!ws || ws_bytes < attention_prefill_workspace_bytes(H, Hkv))
+        return BL_ERR_WORKSPACE;
+    const PrefillArgs a{*q, *k, *v, *out, cu_q, cu_k, batch, H, Hkv, scale, ws, flags};
+    return launch_attention_prefill(a, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+bool valid_rank(int64_t T, int r) { return T >= 1 && T < (int64_t(1) << 31) && r >= 8 && r <= 128 && r % 8 == 0; }
+
+}  // namespace
+
+size_t bitlinear_adapter_workspace_bytes(int64_t T, int r)
+{
+    return valid_rank(T, r) ? adapter_workspace_bytes(T, r) : 0;
+}
+
+int bitlinear_adapter_add(const void *y, int yt, int64_t ldy, const void *x, int64_t ldx,
+                          int64_t T, int64_t N, int64_t K, const void *down, const void *up,
+                          int n, int r, const int32_t *index, const float *scale, void *out,
+                          int64_t ldo, void *ws, size_t ws_bytes, unsigned flags, void *stream)
+{
+    if (!y || !x || !down || !up || !index || !out)
+        return BL_ERR_NULL;
+    if (!valid_dtype(yt))
+        return BL_ERR_DTYPE;
+    if (!valid_nk(N, K) || !valid_rank(T, r) || n < 1 || n > 65536 || ldy < N || ldo < N || ldx < K ||
+        (flags & ~BL_FLAG_PDL) || (out == y && ldo != ldy))
+        return BL_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(down) || !aligned16(up) || ldx * 2 % 16 || !aligned16(ws) ||
+        ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & (yt == BL_BF16 ? 1u : 3u)) ||
+        (reinterpret_cast<uintptr_t>(index) & 3u) || (reinterpret_cast<uintptr_t>(scale) & 3u))
+        return BL_ERR_ALIGN;
+    const DeviceInfo *di;
+    int st = need_device(&di);
+    if (st)
+        return st;
+    if ((st = check_dev_ptrs({y, x, down, up, index, scale, out, ws})))
+        return st;
+    if (!ws || ws_bytes < adapter_workspace_bytes(T, r))
+        return BL_ERR_WORKSPACE;
+    const AdapterArgs a{y, yt, ldy, x, ldx, T, N, K, down, up, n, r, index, scale, out, ldo, ws, flags};
+    return launch_adapter_add(a, static_cast<cudaStream_t>(stream));
+}
+
 size_t bitlinear_chain_plan_bytes(int nsteps) { return chain_plan_bytes(nsteps); }
 
 int bitlinear_chain_plan(int nsteps, const bitlinear_chain_step *steps, void *plan,

@@ -149,6 +149,54 @@ int launch_attention_decode(const void *q, const void *k, const void *v, void *c
                             const float *rope, void *out, void *ws, unsigned flags, cudaStream_t s);
 int launch_position_advance(int32_t *pos, cudaStream_t s);
 
+// Whole prompts and batches of requests: norm + rotation + cache append
+// (qk_norm_rope.cu), causal attention of packed sequences
+// (attention_prefill.cu), low-rank adapters (adapter.cu).
+struct QkNormRopeArgs {
+    bitlinear_heads q, k, v;            // v.data NULL: no values
+    int xt, H, Hkv;
+    const int32_t *positions;
+    const float *table;
+    int64_t table_rows;
+    const void *q_gain, *k_gain;
+    int gt;
+    float eps;
+    const int32_t *slots;
+    bitlinear_heads q_out, k_out, v_out;
+    unsigned flags;
+};
+int launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t s);
+
+constexpr int kPrefillMaxGroup = 64;    // query heads per kv head
+struct PrefillArgs {
+    bitlinear_heads q, k, v, out;
+    const int32_t *cu_q, *cu_k;
+    int batch, H, Hkv;
+    float scale;
+    void *ws;
+    unsigned flags;
+};
+size_t attention_prefill_workspace_bytes(int H, int Hkv);
+int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s);
+
+struct AdapterArgs {
+    const void *y;
+    int yt;
+    int64_t ldy;
+    const void *x;
+    int64_t ldx, T, N, K;
+    const void *down, *up;
+    int n, r;
+    const int32_t *index;
+    const float *scale;
+    void *out;
+    int64_t ldo;
+    void *ws;
+    unsigned flags;
+};
+size_t adapter_workspace_bytes(int64_t T, int r);
+int launch_adapter_add(const AdapterArgs &a, cudaStream_t s);
+
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int launch_gemm(const GemvArgs &a, void *ws, size_t ws_bytes, cudaStream_t s);
 

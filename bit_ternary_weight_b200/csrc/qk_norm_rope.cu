@@ -1,0 +1,210 @@
+// qk_norm_rope.cu -- RMS norm of query and key heads, rotation by the token's
+// position and the write of keys and values to their cache rows, for many
+// tokens in one pass.
+//
+// "bit-floor" README, section "What's inside" (RMSNorm; RoPE on queries and
+// keys before attention).  Per head x of 128 values (all in fp32):
+//   r = 1 / sqrt(mean x^2 + eps),  h = (x * r) * g      (only with a gain)
+//   (a, b) <- (a c - b s, a s + b c)                     (c, s) of the position
+// rounded once to bf16.  The rotation's operations and their order are those
+// of attention.cu, so a prompt's cache rows equal the rows that its tokens
+// would get one at a time.
+//
+// Memory-bound: every element is read once and written once.  Eight lanes
+// take a head, each with dimensions 8c .. 8c + 7 and 64 + 8c .. 64 + 8c + 7, so
+// that every load and store of bf16 is 16 bytes a lane and 128 contiguous
+// bytes a head, and both kinds of pairs ((2i, 2i + 1) and (i, i + 64)) are
+// inside one lane; the mean square is a sum over three shuffles.
+#include "bl_common.cuh"
+
+namespace bl {
+namespace {
+
+constexpr int kHD = 128;
+constexpr int kRopeThreads = 256;
+constexpr int kHeadLanes = 8;
+
+struct RopeParams {
+    const void *q, *k, *v;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    __nv_bfloat16 *qo, *ko, *vo;
+    int64_t qo_row, qo_head, ko_row, ko_head, vo_row, vo_head;
+    int T, H, Hkv, heads;          // heads: H + Hkv (+ Hkv with values)
+    const int32_t *positions;
+    const float2 *table;
+    int64_t table_rows;
+    const void *q_gain, *k_gain;
+    int gt;
+    float eps;
+    const int32_t *slots;
+    int64_t out_rows;
+    int *status;
+};
+
+// Eight gain values (fp32 or bf16).
+__device__ __forceinline__ void gain8(const void *g, int gt, int at, float f[8])
+{
+    if (gt == BL_BF16)
+        load8<BL_BF16, true>(g, at, f);
+    else
+        load8<BL_F32, true>(g, at, f);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    return uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(a))) |
+           uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(b))) << 16;
+}
+
+__device__ __forceinline__ uint4 pack8(const float f[8])
+{
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+__device__ __forceinline__ void rotate(float &a, float &b, float2 cs)
+{
+    const float r0 = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+    const float r1 = __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x));
+    a = r0;
+    b = r1;
+}
+
+template <int XT, bool HALVES>
+__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t item = (int64_t(blockIdx.x) * kRopeThreads + threadIdx.x) / kHeadLanes;
+    const int c = threadIdx.x % kHeadLanes;
+    const int64_t t = item / p.heads;
+    const int h = int(item - t * p.heads);
+    if (t >= p.T)
+        return;     // whole groups of eight lanes; the shuffles below name their group only
+    const unsigned group = 0xffu << (threadIdx.x & 24);
+    const bool is_q = h < p.H, is_k = !is_q && h < p.H + p.Hkv;
+    const int64_t pos = int32_t(ld_dep_u32(p.positions + t));
+    if (pos < 0 || pos >= p.table_rows) {
+        if (h == 0 && c == 0)
+            atomicExch(p.status, BL_ERR_SHAPE);
+        return;
+    }
+    int64_t row = t;
+    if (!is_q && p.slots) {
+        row = int32_t(ld_dep_u32(p.slots + t));
+        if (row < 0)
+            return;
+        if (row >= p.out_rows) {
+            if (c == 0)
+                atomicExch(p.status, BL_ERR_SHAPE);
+            return;
+        }
+    }
+    const int hk = is_q ? h : is_k ? h - p.H : h - p.H - p.Hkv;
+    const void *src = is_q ? p.q : is_k ? p.k : p.v;
+    const int64_t at = is_q ? t * p.q_row + hk * p.q_head : is_k ? t * p.k_row + hk * p.k_head : t * p.v_row + hk * p.v_head;
+    __nv_bfloat16 *dst = is_q   ? p.qo + row * p.qo_row + hk * p.qo_head
+                         : is_k ? p.ko + row * p.ko_row + hk * p.ko_head
+                                : p.vo + row * p.vo_row + hk * p.vo_head;
+    float lo[8], hi[8];
+    load8<XT, true>(src, at + 8 * c, lo);
+    load8<XT, true>(src, at + 64 + 8 * c, hi);
+    if (is_q || is_k) {
+        const void *gain = is_q ? p.q_gain : p.k_gain;
+        if (gain) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], s));
+#pragma unroll
+            for (int o = kHeadLanes / 2; o > 0; o >>= 1)
+                s += __shfl_xor_sync(group, s, o);
+            const float r = __fdiv_rn(1.0f, __fsqrt_rn(s * (1.0f / kHD) + p.eps));
+            float g[8];
+            gain8(gain, p.gt, 8 * c, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                lo[i] = lo[i] * r * g[i];
+            gain8(gain, p.gt, 64 + 8 * c, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                hi[i] = hi[i] * r * g[i];
+        }
+        const float2 *tab = p.table + pos * (kHD / 2);
+        if (HALVES) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                rotate(lo[i], hi[i], __ldcg(tab + 8 * c + i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                rotate(lo[2 * i], lo[2 * i + 1], __ldcg(tab + 4 * c + i));
+                rotate(hi[2 * i], hi[2 * i + 1], __ldcg(tab + 32 + 4 * c + i));
+            }
+        }
+    }
+    *reinterpret_cast<uint4 *>(dst + 8 * c) = pack8(lo);
+    *reinterpret_cast<uint4 *>(dst + 64 + 8 * c) = pack8(hi);
+}
+
+}  // namespace
+
+int launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t s)
+{
+    const DeviceInfo *di = device_info();
+    if (!di)
+        return BL_ERR_CUDA;
+    RopeParams p{};
+    p.q = a.q.data;
+    p.q_row = a.q.row_stride;
+    p.q_head = a.q.head_stride;
+    p.k = a.k.data;
+    p.k_row = a.k.row_stride;
+    p.k_head = a.k.head_stride;
+    p.v = a.v.data;
+    p.v_row = a.v.row_stride;
+    p.v_head = a.v.head_stride;
+    p.qo = static_cast<__nv_bfloat16 *>(a.q_out.data);
+    p.qo_row = a.q_out.row_stride;
+    p.qo_head = a.q_out.head_stride;
+    p.ko = static_cast<__nv_bfloat16 *>(a.k_out.data);
+    p.ko_row = a.k_out.row_stride;
+    p.ko_head = a.k_out.head_stride;
+    p.vo = static_cast<__nv_bfloat16 *>(a.v_out.data);
+    p.vo_row = a.v_out.row_stride;
+    p.vo_head = a.v_out.head_stride;
+    p.T = int(a.q.rows);
+    p.H = a.H;
+    p.Hkv = a.Hkv;
+    p.heads = a.H + a.Hkv + (a.v.data ? a.Hkv : 0);
+    p.positions = a.positions;
+    p.table = reinterpret_cast<const float2 *>(a.table);
+    p.table_rows = a.table_rows;
+    p.q_gain = a.q_gain;
+    p.k_gain = a.k_gain;
+    p.gt = a.gt;
+    p.eps = a.eps;
+    p.slots = a.slots;
+    p.out_rows = a.k_out.rows;
+    p.status = di->status;
+    const int64_t items = int64_t(p.T) * p.heads;
+    const int64_t blocks = (items * kHeadLanes + kRopeThreads - 1) / kRopeThreads;
+    if (blocks > 0x7fffffff)
+        return BL_ERR_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(blocks));
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    if (a.flags & BL_FLAG_PDL) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    const bool halves = a.flags & BL_FLAG_ROPE_HALVES;
+    auto kernel = a.xt == BL_BF16 ? (halves ? qk_norm_rope_kernel<BL_BF16, true> : qk_norm_rope_kernel<BL_BF16, false>)
+                                  : (halves ? qk_norm_rope_kernel<BL_F32, true> : qk_norm_rope_kernel<BL_F32, false>);
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
+}  // namespace bl

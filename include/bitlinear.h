@@ -636,10 +636,139 @@ int bitlinear_probe_mma_i8_issue(int n, int issuers, int reps, long long *out, i
                                  void *stream);
 
 /*
+ * Rows of heads, [rows][heads][128]: element d of head h of row i at
+ * data[i * row_stride + h * head_stride + d] (strides in elements, each row
+ * of 128 contiguous).  A projection's output [T][heads * 128], a part of a
+ * fused one, and a cache [heads][T_max][128] are all of this form.  Every
+ * head starts 16-byte aligned; strides are at least 128 where the size is
+ * above one (a stride of a size of one is not read).
+ */
+typedef struct {
+    void *data;
+    int64_t rows;
+    int64_t row_stride;
+    int64_t head_stride;
+} bitlinear_heads;
+
+/* Flag of bitlinear_qk_norm_rope: a head's pairs are (i, i + 64), not (2i, 2i + 1). */
+#define BL_FLAG_ROPE_HALVES 8u
+
+/*
+ * Queries and keys of T tokens of any number of requests in one pass: RMS
+ * norm of each head (optional), rotation by the token's position, and keys
+ * and values written to their cache rows.  Source: "bit-floor" README,
+ * section "What's inside" (RMSNorm, RoPE on queries and keys before
+ * attention); the many-token form of what bitlinear_attention_decode does
+ * for one token.
+ *   r   = 1 / sqrt(mean_d x[d]^2 + eps)  (the sum in fp32), x <- (x r) g[d]
+ *   (a, b) <- (a c - b s, a s + b c),  (c, s) = table[position][i] for the
+ *         pair (2i, 2i + 1), or (i, i + 64) with BL_FLAG_ROPE_HALVES; the
+ *         products and sums in fp32 in that order, rounded once to bf16.
+ * Without gains this is bit for bit the rotation of bitlinear_attention_decode.
+ *   q, k, v      T rows of H, Hkv, Hkv heads, dtype xt (BL_BF16 or BL_F32); v may
+ *                be NULL together with v_out (keys and queries only)
+ *   positions    device int32 [T]
+ *   table        device fp32 [table_rows][64][2], from bitlinear_rope_table or
+ *                the caller's own; 8-byte aligned
+ *   q_gain,k_gain  NULL (no norm of these heads) or device [128] of dtype gt
+ *   slots        NULL (row t of k_out / v_out for token t) or device int32 [T]:
+ *                token t's row; negative: the token is padding, its key and
+ *                value are written nowhere.  Non-negative slots are distinct.
+ *   q_out        T rows of H heads, bf16;  k_out, v_out: rows of Hkv heads, bf16
+ * The rows of an output do not overlap one another.  An output may be its
+ * input itself (same place, element type and strides; no slots); any other
+ * overlap leaves the overlapping values unspecified.  Rows that no slot names are left as they were.  A
+ * position outside the table or a slot outside k_out records BL_ERR_SHAPE in
+ * the device status word, and nothing is written for that token (position) or
+ * for its key and value (slot).
+ * 1 <= T < 2^31, H, Hkv <= 1024, D == 128.  flags: BL_FLAG_PDL, BL_FLAG_ROPE_HALVES.
+ */
+int bitlinear_qk_norm_rope(const bitlinear_heads *q, const bitlinear_heads *k, const bitlinear_heads *v,
+                           int xt, int H, int Hkv, int D, const int32_t *positions,
+                           const float *table, int64_t table_rows, const void *q_gain,
+                           const void *k_gain, int gt, float eps, const int32_t *slots,
+                           const bitlinear_heads *q_out, const bitlinear_heads *k_out,
+                           const bitlinear_heads *v_out, unsigned flags, void *stream);
+
+/* Bytes of workspace bitlinear_attention_prefill may need for this head
+ * layout on the current device, for any lengths (0 if out of range). */
+size_t bitlinear_attention_prefill_workspace_bytes(int H, int Hkv);
+
+/*
+ * Causal attention of `batch` packed sequences with grouped heads: whole
+ * prompts, pieces of prompts after a cached past, or one new token for each of
+ * many requests.  Source: "How to Run BitNet Inference on GPU Using CUDA
+ * Kernels: A Complete Guide", section "Understanding the Two-Phase
+ * Architecture" (the prefill phase runs Attention over the whole prompt).
+ * Sequence b has the queries cu_q[b] .. cu_q[b + 1] - 1 of q and the keys
+ * cu_k[b] .. cu_k[b + 1] - 1 of k and v, nq and nk of them; its queries are the
+ * last nq of its nk positions: query i sees the keys j <= i + nk - nq.
+ *   s_j = scale * sum_d q[d] K[j][d],  out = sum_j e^(s_j - m) V[j] / sum_j e^(s_j - m)
+ * per query and head (kv head h / (H / Hkv)): products of bf16 on the tensor
+ * cores with fp32 accumulators, running maximum, sum and output in fp32, the
+ * weights rounded to bf16 for their product with V, one rounding to bf16 at
+ * the end.  A query that sees no key (nk < nq, or nk == 0) gets zeros.  Rows of
+ * out outside every sequence are left as they were, and what lies in k and v
+ * outside a sequence's rows, or behind the keys a query sees, has no effect on
+ * that query, NaN and infinities included.  A query that sees a NaN or an
+ * infinity of k or v has an unspecified output.
+ *   q, out       rows of H heads, bf16 (out's rows do not overlap one another, nor q, k or v)
+ *   k, v         rows of Hkv heads, bf16, with the same number of rows; H a multiple of
+ *                Hkv, H / Hkv <= 64; D == 128
+ *   cu_q, cu_k   device int32 [batch + 1], ascending, within the rows of q and k.
+ *                A sequence whose bounds are not records BL_ERR_SHAPE in the
+ *                device status word and writes nothing.
+ *   scale        > 0; 1 / sqrt(128) is usual
+ *   ws, ws_bytes device workspace, 16-byte aligned, of at least
+ *                bitlinear_attention_prefill_workspace_bytes; its contents on
+ *                entry are ignored.  Not shared by calls that can run at the same time.
+ * 1 <= batch <= 65535; q, k with 1 .. 2^31 - 1 rows; strides below 2^38.  flags: BL_FLAG_PDL.
+ */
+int bitlinear_attention_prefill(const bitlinear_heads *q, const bitlinear_heads *k,
+                                const bitlinear_heads *v, const int32_t *cu_q,
+                                const int32_t *cu_k, int batch, int H, int Hkv, int D,
+                                float scale, const bitlinear_heads *out, void *ws,
+                                size_t ws_bytes, unsigned flags, void *stream);
+
+/* Bytes of workspace bitlinear_adapter_add needs for T tokens and rank r on
+ * the current device (0 if out of range). */
+size_t bitlinear_adapter_workspace_bytes(int64_t T, int r);
+
+/*
+ * Low-rank adapters of many requests beside one shared projection:
+ *   out[t] = y[t] + scale[a] * up[a] (down[a] x[t]),  a = index[t]
+ * and out[t] = y[t] where index[t] < 0 (no adapter).  Tokens of different
+ * adapters may come in any order.  The pages have no counterpart: packed
+ * ternary weights are shared and frozen, an adapter is how one request's
+ * model differs from another's.
+ *   y, out       device [T][N] of dtype yt, row pitches ldy, ldo; out may be y
+ *                itself (with ldo == ldy), other overlaps are not allowed
+ *   x            device bf16 [T][K], row pitch ldx: the projection's input
+ *   down         device bf16 [n][r][K];  up: device bf16 [n][N][r]
+ *   index        device int32 [T], below n.  An index at or above n records
+ *                BL_ERR_SHAPE in the device status word; that token's out is y.
+ *   scale        NULL (1) or device fp32 [n]
+ *   ws           device workspace of at least bitlinear_adapter_workspace_bytes;
+ *                contents on entry are ignored.  Not shared by calls that can
+ *                run at the same time.
+ * Both products run on the tensor cores on bf16 operands with fp32
+ * accumulators; the r values between them enter the second as a sum of two
+ * bf16 values (16 bits of mantissa).  Sums have a fixed order: the same call
+ * gives the same bits.
+ * r a multiple of 8, 8 <= r <= 128; K % 64 == 0; x, down and up 16-byte
+ * aligned, ldx such that rows are.  1 <= T < 2^31, 1 <= n <= 65536.  flags: BL_FLAG_PDL.
+ */
+int bitlinear_adapter_add(const void *y, int yt, int64_t ldy, const void *x, int64_t ldx,
+                          int64_t T, int64_t N, int64_t K, const void *down, const void *up,
+                          int n, int r, const int32_t *index, const float *scale, void *out,
+                          int64_t ldo, void *ws, size_t ws_bytes, unsigned flags, void *stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device: BL_OK, BL_ERR_TIMEOUT if a kernel's bounded wait ran out,
  * or BL_ERR_SHAPE if a kernel found a device-side argument out of range (a
- * position outside the KV cache), since the last call.  BL_ERR_CUDA if the
+ * position outside the KV cache or the RoPE table, a cache row, sequence
+ * bounds or an adapter that do not exist), since the last call.  BL_ERR_CUDA if the
  * synchronisation failed.
  */
 int bitlinear_last_device_status(void *stream);
