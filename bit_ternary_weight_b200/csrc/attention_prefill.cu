@@ -1,97 +1,1146 @@
 // attention_prefill.cu -- causal attention of packed sequences with grouped
-// heads.  One warp per (query, head), keys one after the other with a running
-// maximum m and sum l of the softmax:
-//   m' = max(m, s_j), l <- l e^(m - m') + e^(s_j - m'), o <- o e^(m - m') + e^(s_j - m') V[j]
-#include "bl_common.cuh"
+// heads on the sm_100a tensor cores: whole prompts, pieces of prompts behind a
+// cached past, single tokens of many requests.
+//
+// "How to Run BitNet Inference on GPU Using CUDA Kernels: A Complete Guide",
+// section "Understanding the Two-Phase Architecture" (the prefill phase runs
+// Attention over the whole prompt).
+//
+// Mathematics.  For a block of keys with scores S = q K^T (fp32), a reference
+// maximum m and c = scale * log2(e):
+//   P = 2^(c S - c m),  l <- l + sum P,  O <- O + P V
+// m starts as the first block's maximum and moves only when a later block's
+// exceeds it by more than 8 / c: then O and l are multiplied by 2^(c (m - m')).
+// Until then P stays below 2^8, which fp32 sums and bf16 weights hold as well
+// as values below 1, and the pass over O is saved.  out = O / l.
+//
+// Rows.  The query heads of a kv head share its keys, so a tile's 128 rows are
+// (token, head of the group): TM = 128 / G tokens of G heads.  A tile of one
+// token and a long cache is then G rows against one pass over the keys, and a
+// prompt's tile spans few tokens, so little of its last key blocks is masked.
+//
+// Two streams.  A CTA keeps two rows of products going, each with its own S
+// and O in tensor memory (4 x 128 columns), its own four softmax warps (a
+// thread per row), and P written over S as the next product's operand:
+//   pair  two tiles of rows share every key block (prompts: each block of K
+//         and V is read once for 256 rows);
+//   alt   one tile, key blocks alternate between the streams, whose results
+//         are merged at the end (few rows: two blocks are in flight).
+// While one stream's warps compute exponentials, the tensor cores run the
+// other's products.
+//
+// Work.  The key blocks of all tiles form one line; CTA c takes the c-th of
+// equal parts of it, whatever the sequences' lengths.  A tile that is cut has
+// its parts' O, m and l (fp32) in the workspace, and a second kernel joins
+// them in order.  Each CTA cuts at most two tiles, one at either end.
+//
+// Warp roles (384 threads; warp 11 idles):
+//   warps 0-3, 4-7  softmax of streams 0 and 1, a row per thread; epilogue
+//   warp 8          work list and TMA loads (Q, then K and V blocks in a ring)
+//   warp 9          MMA issue (lane 0, the whole warp in uniform control flow)
+//   warp 10         values behind a mask: in blocks where some row's keys are
+//                   masked, non-finite values of V are zeroed before the
+//                   product (a zero weight times a NaN would reach rows that
+//                   do not see it) and rows that do see them get NaN.
+//
+// Every mbarrier wait is bounded (2 s); on expiry BL_ERR_TIMEOUT is recorded,
+// every role leaves its loop, copies and MMAs in flight drain, tensor memory
+// is freed and the CTA returns.
+#include <algorithm>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "tcgen05_common.cuh"
 
 namespace bl {
 namespace {
 
-constexpr int kHD = 128;
+constexpr int kHD = 128;                  // head dimension
+constexpr int kRows = 128;                // rows per tile (MMA M)
+constexpr int kKeys = 128;                // keys per block (MMA N of the scores)
+constexpr int kThreads = 384;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10;
+constexpr uint32_t kBox = 128 * 128;      // 64 columns x 128 rows of bf16, one swizzle span wide
+constexpr uint32_t kTile = 2 * kBox;      // 128 x 128 bf16
+constexpr int kItems = 4;                 // work list ring
+constexpr float kRescale = 8.0f;          // log2 of the growth of a row's weights before O is rescaled
+// Registers: 168 a thread at launch; a softmax thread holds its row of S.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+
+// Instruction descriptors: D fp32, A and B bf16, M = N = 128; B is K-major for
+// the scores (keys x dimensions) and MN-major for the values (the same tile,
+// dimensions as N).
+constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kKeys >> 3) << 17) |
+                              (uint32_t(kRows >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+
+template <bool PAIR>
+constexpr int kv_stages() { return PAIR ? 5 : 6; }
+
+// One piece of work: key blocks [j0, j1) of a tile of rows.
+struct Item {
+    int valid;
+    int kvh;                // kv head
+    int q_row, toks;        // first row of q and tokens of the tile
+    int lim0, nk;           // token i of the tile sees the keys below min(nk, lim0 + i)
+    int k_row;              // first key row of the sequence
+    int j0, n;              // first key block, number of blocks (0: no row sees a key)
+    int nb[2];              // blocks of each stream
+    int slot;               // workspace slot, -1: the tile is whole
+};
+
+// What the joining kernel needs about the tile whose first part a CTA holds.
+struct JoinHeader {
+    int valid;
+    int kvh, q_row, toks;
+    int last;               // CTA of the last part
+    int pad[3];
+};
 
 struct PrefillParams {
-    const __nv_bfloat16 *q, *k, *v;
     __nv_bfloat16 *out;
-    int64_t q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;
+    int64_t o_row, o_head;
     const int32_t *cu_q, *cu_k;
-    int batch, H, group;
+    int batch, Hkv, G, TM;
     int64_t Tq, Tk;
-    float scale;
+    float c;                // scale * log2(e)
+    JoinHeader *hdr;        // [grid]
+    float *part_o;          // [2 * grid][rows][128]
+    float2 *part_ml;        // [2 * grid][rows]
     int *status;
 };
 
-__device__ __forceinline__ void load4(const __nv_bfloat16 *src, float f[4])
+template <bool PAIR>
+struct Smem {
+    static constexpr int kStages = kv_stages<PAIR>();
+    static constexpr int kQTiles = PAIR ? 2 : 1;
+    unsigned char q[kQTiles][kTile];
+    unsigned char kv[kStages][kTile];
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t v_posted[kStages];      // a block that needs fixing has been asked for in this stage
+    uint64_t v_fixed[kStages];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2];      // scores complete (and every earlier product)
+    uint64_t p_full[2];      // weights written over the scores
+    uint64_t o_full[2];      // last product of the piece complete
+    uint64_t ml_full;        // alt: stream 1's m and l are in ml
+    uint64_t o1_read;        // alt: stream 1's O has been read
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t drain;
+    Item item[kItems];
+    float2 ml[PAIR ? 1 : kRows];
+    int poison_piece;        // piece that poison is about
+    int poison[kHD];         // first key with a non-finite value in this dimension
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <bool PAIR>
+constexpr uint32_t smem_bytes() { return uint32_t(sizeof(Smem<PAIR>)); }
+static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1024, "shared memory per CTA");
+static_assert(smem_bytes<true>() > 114 * 1024 && smem_bytes<false>() > 114 * 1024,
+              "one CTA per SM: it owns all of the tensor memory");
+
+// ---------------------------------------------------------------- PTX wrappers
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2)
 {
-    const uint2 w = *reinterpret_cast<const uint2 *>(src);
-    f[0] = __uint_as_float(w.x << 16);
-    f[1] = __uint_as_float(w.x & 0xffff0000u);
-    f[2] = __uint_as_float(w.y << 16);
-    f[3] = __uint_as_float(w.y & 0xffff0000u);
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
 }
 
-__global__ void __launch_bounds__(128) prefill_kernel(const PrefillParams p)
+// K-major and MN-major operands share the stride between 8-row groups; the
+// latter also has a stride between its 64-column boxes.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr)
 {
+    return (smem_desc_sw128(addr) & ~(uint64_t(0x3fff) << 16)) | (uint64_t(kBox >> 4) << 16);
+}
+
+// Scores of one key block: eight MMAs over the 128 dimensions, operands in
+// shared memory, four in each 64-column box.
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b)
+{
+    constexpr uint32_t box = kBox >> 4;
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 r;\n\t"
+        "mov.u32 r, %%laneid;\n\t"
+        "setp.eq.u32 e, r, 0;\n\t"
+        "setp.ne.b32 p, %18, %18;\n\t"
+        "setp.eq.b32 t, %18, %18;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %9, %17, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %10, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %11, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %12, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %13, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %6, %14, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %15, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %8, %16, %17, t;\n\t}" ::"r"(d),
+        "l"(a), "l"(a + 2), "l"(a + 4), "l"(a + 6), "l"(a + box), "l"(a + box + 2), "l"(a + box + 4),
+        "l"(a + box + 6), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "l"(b + box), "l"(b + box + 2),
+        "l"(b + box + 4), "l"(b + box + 6), "r"(kIdescQK), "r"(0u)
+        : "memory");
+}
+
+// Weights (tensor memory) times values: eight MMAs over the 128 keys, 16 keys
+// (two 8-row groups, 2048 bytes) each.
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 r;\n\t"
+        "mov.u32 r, %%laneid;\n\t"
+        "setp.eq.u32 e, r, 0;\n\t"
+        "setp.ne.b32 p, %18, 0;\n\t"
+        "setp.eq.b32 t, %18, %18;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %9, %17, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %10, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %11, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %12, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %13, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%6], %14, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %15, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%8], %16, %17, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "r"(a + 32), "r"(a + 40), "r"(a + 48), "r"(a + 56), "l"(b),
+        "l"(b + 128), "l"(b + 256), "l"(b + 384), "l"(b + 512), "l"(b + 640), "l"(b + 768), "l"(b + 896),
+        "r"(kIdescPV), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---------------------------------------------------------------- the work line
+
+// Bounds of sequence b; false if they are not ascending and within the rows.
+__device__ __forceinline__ bool sequence(const PrefillParams &p, int b, int &q0, int &nq, int &k0, int &nk)
+{
+    q0 = int(ld_dep_u32(p.cu_q + b));
+    const int q1 = int(ld_dep_u32(p.cu_q + b + 1));
+    k0 = int(ld_dep_u32(p.cu_k + b));
+    const int k1 = int(ld_dep_u32(p.cu_k + b + 1));
+    const bool ok = q0 >= 0 && q1 >= q0 && int64_t(q1) <= p.Tq && k0 >= 0 && k1 >= k0 && int64_t(k1) <= p.Tk;
+    nq = ok ? q1 - q0 : 0;
+    nk = ok ? k1 - k0 : 0;
+    return ok;
+}
+
+// Key blocks that the tile of `tt` tokens from token t0 of a sequence covers.
+__device__ __forceinline__ int tile_blocks(int t0, int tt, int nq, int nk)
+{
+    const int64_t seen = int64_t(min(int64_t(nq), int64_t(t0) + tt)) + nk - nq;
+    return seen <= 0 ? 0 : int((seen + kKeys - 1) / kKeys);
+}
+
+// The same in units of the work line: a tile without keys still is one.
+__device__ __forceinline__ int64_t head_units(int tt, int nq, int nk)
+{
+    int64_t u = 0;
+    for (int64_t t0 = 0; t0 < nq; t0 += tt)
+        u += max(1, tile_blocks(int(t0), tt, nq, nk));
+    return u;
+}
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// ---------------------------------------------------------------- kernel
+
+// mbar_wait without a call: a kernel that moves registers between its warps
+// (setmaxnreg) cannot hold one, since a callee's registers are not bounded.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                            uint64_t limit_ns = kWaitLimitNs)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    for (;;) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (abort_flag && *abort_flag)
+            return false;
+        if (global_timer_ns() - t0 > limit_ns) {
+            if (abort_flag)
+                *abort_flag = 1;
+            atomicExch(status, BL_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+constexpr uint64_t kDrainLimitNs = 100000000ull;
+
+// Waits that give up return false; a warp acts on its lanes' common outcome.
+#define BL_WAIT(bar, parity) __all_sync(0xffffffffu, wait_inline(smem_u32(&(bar)), (parity), abort_flag, p.status))
+
+template <bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+               const __grid_constant__ CUtensorMap vmap, const PrefillParams p)
+{
+    constexpr int kStages = kv_stages<PAIR>();
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Smem<PAIR> &sm = *reinterpret_cast<Smem<PAIR> *>(smem_raw);
+    // the swizzled tiles begin at multiples of 1024 bytes, as declared (there
+    // is no room to align by hand)
+    if (smem_u32(smem_raw) & 1023u) {
+        if (threadIdx.x == 0)
+            atomicExch(p.status, BL_ERR_UNSUPPORTED);
+        return;
+    }
+    volatile int *abort_flag = &sm.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&sm.kv_full[s]), 1);
+            mbar_init(smem_u32(&sm.kv_empty[s]), 1);
+            mbar_init(smem_u32(&sm.v_posted[s]), 1);
+            mbar_init(smem_u32(&sm.v_fixed[s]), 32);
+        }
+        mbar_init(smem_u32(&sm.q_full), 1);
+        mbar_init(smem_u32(&sm.q_empty), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&sm.s_full[s]), 1);
+            mbar_init(smem_u32(&sm.p_full[s]), 128);
+            mbar_init(smem_u32(&sm.o_full[s]), 1);
+        }
+        mbar_init(smem_u32(&sm.ml_full), 128);
+        mbar_init(smem_u32(&sm.o1_read), 128);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(smem_u32(&sm.item_full[i]), 1);
+            mbar_init(smem_u32(&sm.item_empty[i]), 10);     // a lane of each of the other warps
+        }
+        mbar_init(smem_u32(&sm.drain), 1);
+        sm.abort_flag = 0;
+        sm.poison_piece = -1;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+    }
+    if (warp == kMmaWarp)
+        tmem_alloc(smem_u32(&sm.tmem_base), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.batch; b += 128)
-            if (p.cu_q[b] < 0 || p.cu_q[b + 1] < p.cu_q[b] || int64_t(p.cu_q[b + 1]) > p.Tq || p.cu_k[b] < 0 ||
-                p.cu_k[b + 1] < p.cu_k[b] || int64_t(p.cu_k[b + 1]) > p.Tk)
+
+    if (warp >= kLoadWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kLoadWarp) {
+            // ---------------------------------------- work list, TMA loads
+            const int TT = PAIR ? 2 * p.TM : p.TM;        // tokens of a tile
+            int64_t W = 0;
+            bool bad = false;
+            for (int b0 = 0; b0 < p.batch; b0 += 32) {
+                int q0, nq = 0, k0, nk = 0;
+                if (b0 + lane < p.batch) {
+                    bad |= !sequence(p, b0 + lane, q0, nq, k0, nk);
+                    W += head_units(TT, nq, nk);
+                }
+            }
+            W = warp_sum64(W) * p.Hkv;
+            if (bad && blockIdx.x == 0)
                 atomicExch(p.status, BL_ERR_SHAPE);
-    const int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int64_t t = item / p.H;
-    const int h = int(item - t * p.H);
-    if (t >= p.Tq)
-        return;
-    int64_t q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-    for (int b = 0; b < p.batch && !(q0 <= t && t < q1); ++b) {
-        q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
-        if (q0 < 0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk)
-            q1 = q0;        // reported above
-    }
-    if (t < q0 || t >= q1)
-        return;
-    const int64_t seen = (k1 - k0) - (q1 - 1 - t);      // keys below this are visible
-    float q[4], o[4] = {};
-    load4(p.q + t * p.q_row + h * p.q_head + 4 * lane, q);
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t j = 0; j < seen; ++j) {
-        float k[4], v[4];
-        load4(p.k + (k0 + j) * p.k_row + h / p.group * p.k_head + 4 * lane, k);
-        load4(p.v + (k0 + j) * p.v_row + h / p.group * p.v_head + 4 * lane, v);
-        const float s = p.scale * warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]);
-        const float m1 = fmaxf(m, s), f = expf(m - m1), e = expf(s - m1);
-        m = m1;
-        l = l * f + e;
+            const int64_t G = min(int64_t(gridDim.x), W), c = blockIdx.x;
+            int64_t w = c < G ? c * W / G : 0;            // the next unit of this CTA, its end
+            const int64_t w_end = c < G ? (c + 1) * W / G : 0;
+            // the sequence that holds unit w
+            int b = 0, q0 = 0, nq = 0, k0 = 0, nk = 0, kvh = 0, t0 = 0;
+            int64_t off = w;                              // units from the tile's first to w
+            if (w < w_end) {
+                int64_t before = 0;
+                for (int b0 = 0; b0 < p.batch; b0 += 32) {
+                    int a0, a1 = 0, a2, a3 = 0;
+                    int64_t u = 0;
+                    if (b0 + lane < p.batch) {
+                        sequence(p, b0 + lane, a0, a1, a2, a3);
+                        u = head_units(TT, a1, a3) * p.Hkv;
+                    }
+                    int64_t incl = u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = o[i] * f + e * v[i];
-    }
-    __nv_bfloat16 *dst = p.out + t * p.o_row + h * p.o_head + 4 * lane;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                        incl += lane >= o ? v : 0;
+                    }
+                    const unsigned past = __ballot_sync(0xffffffffu, before + incl > w);
+                    if (past) {
+                        const int l = __ffs(past) - 1;
+                        b = b0 + l;
+                        off = w - (before + __shfl_sync(0xffffffffu, incl - u, l));
+                        break;
+                    }
+                    before += __shfl_sync(0xffffffffu, incl, 31);
+                }
+                sequence(p, b, q0, nq, k0, nk);
+                const int64_t per_head = head_units(TT, nq, nk);
+                kvh = int(off / per_head);
+                off -= kvh * per_head;
+                for (;;) {
+                    const int u = max(1, tile_blocks(t0, TT, nq, nk));
+                    if (off < u)
+                        break;
+                    off -= u;
+                    t0 += TT;
+                }
+            }
+            if (lane == 0)
+                p.hdr[c].valid = 0;
+            int it = 0, loads = 0;       // pieces listed, blocks loaded
+            int q_loads = 0;
+            bool ok = true;
+            for (; ok; ++it) {
+                const int islot = it % kItems;
+                if (!BL_WAIT(sm.item_empty[islot], (uint32_t(it / kItems) & 1u) ^ 1u))
+                    break;
+                Item item = {};
+                if (w < w_end) {
+                    const int blocks = tile_blocks(t0, TT, nq, nk), units = max(1, blocks);
+                    const int take = int(min(int64_t(units) - off, w_end - w));
+                    item.valid = 1;
+                    item.kvh = kvh;
+                    item.q_row = q0 + t0;
+                    item.toks = min(TT, nq - t0);
+                    item.lim0 = int(max(int64_t(-0x40000000), int64_t(t0) + 1 + nk - nq));
+                    item.nk = nk;
+                    item.k_row = k0;
+                    item.j0 = int(off);
+                    item.n = blocks ? take : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        dst[i] = __float2bfloat16_rn(seen > 0 ? o[i] / l : 0.0f);
+                    for (int s = 0; s < 2; ++s) {
+                        if (PAIR) {
+                            const int rows = min(item.toks - s * p.TM, p.TM);
+                            const int kb = rows <= 0 ? 0 : tile_blocks(t0 + s * p.TM, rows, nq, nk);
+                            item.nb[s] = max(0, min(item.j0 + item.n, kb) - item.j0);
+                        } else {
+                            item.nb[s] = (item.n + 1 - s) / 2;
+                        }
+                    }
+                    item.slot = take == units ? -1 : off ? 2 * int(c) : 2 * int(c) + 1;
+                    if (off == 0 && take < units && lane == 0) {
+                        // the CTA that holds unit w + units - 1
+                        const int64_t last = ((w + units) * G + W - 1) / W - 1;
+                        p.hdr[c] = JoinHeader{1, kvh, item.q_row, item.toks, int(last), {}};
+                    }
+                    w += take;
+                    off += take;
+                    if (off == units) {
+                        off = 0;
+                        t0 += TT;
+                        if (t0 >= nq) {
+                            t0 = 0;
+                            if (++kvh == p.Hkv) {
+                                kvh = 0;
+                                if (w < w_end) {
+                                    do
+                                        sequence(p, ++b, q0, nq, k0, nk);
+                                    while (nq == 0);
+                                }
+                            }
+                        }
+                    }
+                }
+                if (lane == 0) {
+                    sm.item[islot] = item;
+                    mbar_arrive(smem_u32(&sm.item_full[islot]));
+                }
+                __syncwarp();
+                if (!item.valid)
+                    break;
+                if (item.n == 0)
+                    continue;
+                // queries (once every score product of the previous piece is complete)
+                if (!BL_WAIT(sm.q_empty, (uint32_t(q_loads) & 1u) ^ 1u))
+                    break;
+                ++q_loads;
+                const int qt = PAIR && item.toks > p.TM ? 2 : 1;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&sm.q_full);
+                    mbar_arrive_tx(bar, uint32_t(qt * p.TM * p.G) * 256u);
+                    for (int s = 0; s < qt; ++s) {
+                        const uint32_t dst = smem_u32(sm.q[s]);
+                        tma_load_3d(dst, &qmap, bar, 0, item.kvh * p.G, item.q_row + s * p.TM);
+                        tma_load_3d(dst + kBox, &qmap, bar, 64, item.kvh * p.G, item.q_row + s * p.TM);
+                    }
+                }
+                __syncwarp();
+                // blocks in the order in which the products take them
+                const int n = item.n, masked = max(0, min(item.nk, item.lim0)) / kKeys - item.j0;
+                for (int x = 0; x < 2 * n; ++x, ++loads) {
+                    bool is_v;
+                    int i;
+                    if (PAIR) {
+                        is_v = x & 1;
+                        i = x >> 1;
+                    } else if (x < min(2, n)) {
+                        is_v = false;
+                        i = x;
+                    } else {
+                        // V(0), K(2), V(1), K(3), ..., V(n - 2), V(n - 1)
+                        const int y = x - min(2, n);
+                        is_v = !(y & 1) || y > 2 * (n - 2);
+                        i = y > 2 * (n - 2) ? y - max(0, n - 2) : is_v ? y / 2 : y / 2 + 2;
+                    }
+                    const int st = loads % kStages;
+                    if (!BL_WAIT(sm.kv_empty[st], (uint32_t(loads / kStages) & 1u) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const uint32_t bar = smem_u32(&sm.kv_full[st]), dst = smem_u32(sm.kv[st]);
+                        const CUtensorMap *map = is_v ? &vmap : &kmap;
+                        const int row = item.k_row + (item.j0 + i) * kKeys;
+                        mbar_arrive_tx(bar, kTile);
+                        tma_load_3d(dst, map, bar, 0, item.kvh, row);
+                        tma_load_3d(dst + kBox, map, bar, 64, item.kvh, row);
+                        if (is_v && i >= masked)
+                            mbar_arrive(smem_u32(&sm.v_posted[st]));
+                    }
+                    __syncwarp();
+                }
+            }
+            // copies in flight have landed before the CTA exits (at once
+            // unless another role gave up before it took them)
+            for (int x = max(0, loads - kStages); x < loads; ++x)
+                wait_inline(smem_u32(&sm.kv_full[x % kStages]), uint32_t(x / kStages) & 1u, nullptr, p.status,
+                            kDrainLimitNs);
+            if (q_loads)
+                wait_inline(smem_u32(&sm.q_full), uint32_t(q_loads - 1) & 1u, nullptr, p.status, kDrainLimitNs);
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------- MMA issue
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[0]));
+            const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.kv[0]));
+            const uint64_t v_desc = smem_desc_mn_sw128(smem_u32(sm.kv[0]));
+            int loads = 0, q_loads = 0;
+            uint32_t fixed_parity = 0;              // bit per stage
+            uint32_t p_parity[2] = {0, 0};
+            bool ok = true, issued = false;
+            // wait for load x
+            auto landed = [&](int x) { return BL_WAIT(sm.kv_full[x % kStages], uint32_t(x / kStages) & 1u); };
+            auto scores = [&](int s, int x) {
+                tc_fence_after();
+                mma_scores(tmem + uint32_t(s * kKeys), q_desc + uint64_t(PAIR ? s : 0) * (kTile >> 4),
+                           k_desc + uint64_t(x % kStages) * (kTile >> 4));
+                mma_commit(smem_u32(&sm.s_full[s]));
+            };
+            // O += P V of stream s; the products run in the order of their
+            // issue, so the next scores may follow over P at once
+            auto values = [&](int s, int x, bool first) {
+                if (!BL_WAIT(sm.p_full[s], p_parity[s]))
+                    return false;
+                p_parity[s] ^= 1u;
+                tc_fence_after();
+                mma_values(tmem + uint32_t(256 + s * kHD), tmem + uint32_t(s * kKeys),
+                           v_desc + uint64_t(x % kStages) * (kTile >> 4), first ? 0u : 1u);
+                return true;
+            };
+            for (int it = 0; ok; ++it) {
+                const int islot = it % kItems;
+                if (!BL_WAIT(sm.item_full[islot], uint32_t(it / kItems) & 1u))
+                    break;
+                const int valid = sm.item[islot].valid, n = sm.item[islot].n, j0 = sm.item[islot].j0;
+                const int nb0 = sm.item[islot].nb[0], nb1 = sm.item[islot].nb[1];
+                const int full = max(0, min(sm.item[islot].nk, sm.item[islot].lim0)) / kKeys;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm.item_empty[islot]));
+                if (!valid)
+                    break;
+                if (n == 0)
+                    continue;
+                if (!BL_WAIT(sm.q_full, uint32_t(q_loads) & 1u))
+                    break;
+                ++q_loads;
+                issued = true;
+                // V of block i is complete, with non-finite values behind masks removed
+                auto v_ready = [&](int x, int i) {
+                    if (!landed(x))
+                        return false;
+                    if (j0 + i >= full) {
+                        const int st = x % kStages;
+                        if (!BL_WAIT(sm.v_fixed[st], (fixed_parity >> st) & 1u))
+                            return false;
+                        fixed_parity ^= 1u << st;
+                    }
+                    return true;
+                };
+                if (PAIR) {
+                    if (!landed(loads))
+                        break;
+                    if (nb0)
+                        scores(0, loads);
+                    if (nb1)
+                        scores(1, loads);
+                    if (n == 1)
+                        mma_commit(smem_u32(&sm.q_empty));
+                    mma_commit(smem_u32(&sm.kv_empty[loads % kStages]));
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int xv = loads + 2 * i + 1, xk = xv + 1;
+                        ok = v_ready(xv, i);
+                        bool k_here = false;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int nb = s ? nb1 : nb0;
+                            if (!ok || i >= nb)
+                                continue;
+                            ok = values(s, xv, i == 0);
+                            if (ok && i + 1 < nb) {
+                                ok = k_here || landed(xk);
+                                k_here = true;
+                                if (ok)
+                                    scores(s, xk);
+                            } else if (ok) {
+                                mma_commit(smem_u32(&sm.o_full[s]));
+                            }
+                        }
+                        if (!ok)
+                            break;
+                        mma_commit(smem_u32(&sm.kv_empty[xv % kStages]));
+                        if (i + 1 < n) {
+                            ok = k_here || landed(xk);
+                            mma_commit(smem_u32(&sm.kv_empty[xk % kStages]));
+                            if (i + 2 == n)
+                                mma_commit(smem_u32(&sm.q_empty));
+                        }
+                    }
+                } else {
+                    for (int i = 0; i < min(2, n) && ok; ++i) {
+                        ok = landed(loads + i);
+                        if (ok) {
+                            scores(i, loads + i);
+                            if (i + 1 == n)
+                                mma_commit(smem_u32(&sm.q_empty));
+                            mma_commit(smem_u32(&sm.kv_empty[(loads + i) % kStages]));
+                        }
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int xv = loads + i + min(n, i + 2), s = i & 1;
+                        ok = v_ready(xv, i);
+                        if (ok)
+                            ok = s ? values(1, xv, i < 2) : values(0, xv, i < 2);
+                        if (!ok)
+                            break;
+                        mma_commit(smem_u32(&sm.kv_empty[xv % kStages]));
+                        if (i + 2 < n) {
+                            ok = landed(xv + 1);
+                            if (!ok)
+                                break;
+                            scores(s, xv + 1);
+                            mma_commit(smem_u32(&sm.kv_empty[(xv + 1) % kStages]));
+                            if (i + 3 == n)
+                                mma_commit(smem_u32(&sm.q_empty));
+                        } else {
+                            mma_commit(smem_u32(&sm.o_full[s]));
+                        }
+                    }
+                }
+                loads += 2 * n;
+            }
+            if (issued) {
+                // every MMA has completed before tensor memory is released
+                mma_commit(smem_u32(&sm.drain));
+                wait_inline(smem_u32(&sm.drain), 0, nullptr, p.status, kDrainLimitNs);
+            }
+        } else if (warp == kFixWarp) {
+            // ---------------------------------------- non-finite values behind masks
+            int loads = 0;
+            uint32_t posted_parity = 0;             // bit per stage
+            bool ok = true;
+            for (int it = 0; ok; ++it) {
+                const int islot = it % kItems;
+                if (!BL_WAIT(sm.item_full[islot], uint32_t(it / kItems) & 1u))
+                    break;
+                const int valid = sm.item[islot].valid, n = sm.item[islot].n, j0 = sm.item[islot].j0;
+                const int nk = sm.item[islot].nk;
+                const int full = max(0, min(nk, sm.item[islot].lim0)) / kKeys;
+                for (int i = max(0, full - j0); i < n && ok && valid; ++i) {
+                    const int x = loads + (PAIR ? 2 * i + 1 : i + min(n, i + 2)), st = x % kStages;
+                    // this warp passes over the other blocks, so the stage's
+                    // phase is the block's only once it has been asked for
+                    ok = BL_WAIT(sm.v_posted[st], (posted_parity >> st) & 1u) &&
+                         BL_WAIT(sm.kv_full[st], uint32_t(x / kStages) & 1u);
+                    if (!ok)
+                        break;
+                    posted_parity ^= 1u << st;
+                    // bf16 with all exponent bits set: exponent + 1 carries into the sign's place
+                    uint4 *tile = reinterpret_cast<uint4 *>(sm.kv[st]);
+                    uint32_t hit = 0;
+#pragma unroll 8
+                    for (int u = 0; u < int(kTile / 16) / 32; ++u) {
+                        const uint4 v = tile[u * 32 + lane];
+                        hit |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                               ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+                    }
+                    if (__any_sync(0xffffffffu, hit & 0x80008000u)) {
+                        // rare: zero them, and note for each dimension the first
+                        // key of the sequence whose value was not finite.  The
+                        // notes of the previous piece have been read once both
+                        // softmax groups have left it.
+                        if (sm.poison_piece != it) {
+                            if (it > 0 &&
+                                !BL_WAIT(sm.item_empty[(it - 1) % kItems], uint32_t((it - 1) / kItems) & 1u)) {
+                                ok = false;
+                                break;
+                            }
+                            for (int d = lane; d < kHD; d += 32)
+                                sm.poison[d] = 0x7fffffff;
+                            __syncwarp();
+                        }
+                        for (int e = lane; e < int(kTile / 2); e += 32) {      // in memory order
+                            unsigned short *q = reinterpret_cast<unsigned short *>(sm.kv[st]) + e;
+                            if ((*q & 0x7f80u) == 0x7f80u) {
+                                const int row = (e >> 6) & 127;                // key of the block
+                                const int chunk = ((e >> 3) & 7) ^ (row & 7);  // the swizzle undone
+                                const int d = (e >> 13) * 64 + chunk * 8 + (e & 7);
+                                const int key = (j0 + i) * kKeys + row;
+                                if (key < nk)
+                                    atomicMin(&sm.poison[d], key);
+                                *q = 0;
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0)
+                            sm.poison_piece = it;
+                        __syncwarp();
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    mbar_arrive(smem_u32(&sm.v_fixed[st]));
+                }
+                loads += 2 * n;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm.item_empty[islot]));
+                if (!valid)
+                    break;
+            }
+        }
+    } else {
+        // -------------------------------------------- softmax, one row per thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int s = warp >> 2;                            // stream
+        const int r = threadIdx.x & 127;                    // row of the tile
+        const uint32_t lanes = uint32_t(warp & 3) << 21;    // TMEM lanes 32 * (warp % 4) ..
+        const uint32_t s_tmem = tmem + lanes + uint32_t(s * kKeys), o_tmem = tmem + lanes + uint32_t(256 + s * kHD);
+        const int tok = r / p.G, g = r - tok * p.G;         // of the tile's rows
+        uint32_t s_parity = 0, o_parity[2] = {0, 0}, ml_parity = 0, o1_parity = 0;
+        bool o1_pending = false;                            // alt, stream 1: its last O may still be read
+        for (int it = 0;; ++it) {
+            const int islot = it % kItems;
+            if (!BL_WAIT(sm.item_full[islot], uint32_t(it / kItems) & 1u))
+                break;
+            const Item &item = sm.item[islot];
+            if (!item.valid)
+                break;
+            const int tt = (PAIR ? s * p.TM : 0) + tok;     // token of the tile
+            const bool mine = tok < p.TM && tt < item.toks;
+            const int limit = min(item.nk, item.lim0 + tt); // keys below are visible
+            const int nb = item.nb[s];
+            // blocks before this one are visible to every row of the stream
+            const int full = max(0, min(item.nk, item.lim0 + (PAIR ? s * p.TM : 0))) / kKeys;
+            float m = -INFINITY, l = 0.0f;
+            bool ok = true;
+            for (int i = 0; i < nb; ++i) {
+                const int j = item.j0 + (PAIR ? i : 2 * i + s);
+                if (!PAIR && i == 0 && o1_pending) {
+                    // the product that the first weights release overwrites O
+                    ok = BL_WAIT(sm.o1_read, o1_parity);
+                    if (!ok)
+                        break;
+                    o1_parity ^= 1u;
+                    o1_pending = false;
+                }
+                ok = BL_WAIT(sm.s_full[s], s_parity);
+                if (!ok)
+                    break;
+                s_parity ^= 1u;
+                tc_fence_after();
+                uint32_t v[128];
+                tmem_ld128_wait(s_tmem, v);
+                if (j >= full) {
+                    const int left = limit - j * kKeys;
+#pragma unroll
+                    for (int x = 0; x < 128; ++x)
+                        v[x] = x < left ? v[x] : 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mx[x] = __uint_as_float(v[x]);
+#pragma unroll
+                for (int x = 4; x < 128; ++x)
+                    mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(v[x]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (i == 0) {
+                    m = top;
+                } else {
+                    const bool grow = (top - m) * p.c > kRescale;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? exp2_approx((m - top) * p.c) : 1.0f;
+                        m = grow ? top : m;
+                        l *= f;
+                        // the scores' barrier covers every earlier product: O is idle
+#pragma unroll 1
+                        for (int x = 0; x < kHD; x += 32) {
+                            uint32_t o[32];
+                            tmem_ld32_wait(o_tmem + uint32_t(x), o);
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                            tmem_st32_wait(o_tmem + uint32_t(x), o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.0f : m * p.c;
+                float sum[4] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const float a = exp2_approx(fmaf(__uint_as_float(v[64 * h + 2 * x]), p.c, -mc));
+                        const float b = exp2_approx(fmaf(__uint_as_float(v[64 * h + 2 * x + 1]), p.c, -mc));
+                        sum[x & 1] += a;
+                        sum[2 + (x & 1)] += b;
+                        w[x] = bf16x2(a, b);
+                    }
+                    tmem_st32_wait(s_tmem + uint32_t(32 * h), w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sm.p_full[s]));
+            }
+            if (!ok)
+                break;
+            // ---- the piece's result: f0 * O of this stream (+ f1 * O of stream 1, alt)
+            float f0 = 1.0f, f1 = 0.0f;
+            bool second = false;
+            if (!PAIR && s == 1) {
+                if (nb) {
+                    sm.ml[r] = make_float2(m, l);
+                    mbar_arrive(smem_u32(&sm.ml_full));
+                    o1_pending = true;
+                }
+            } else {
+                if (nb) {
+                    if (!BL_WAIT(sm.o_full[s], o_parity[0]))
+                        break;
+                    o_parity[0] ^= 1u;
+                }
+                if (!PAIR && item.nb[1]) {
+                    if (!BL_WAIT(sm.ml_full, ml_parity) || !BL_WAIT(sm.o_full[1], o_parity[1]))
+                        break;
+                    ml_parity ^= 1u;
+                    o_parity[1] ^= 1u;
+                    second = true;
+                    const float2 ml1 = sm.ml[r];
+                    const float top = fmaxf(m, ml1.x);
+                    f0 = m == -INFINITY ? 0.0f : exp2_approx((m - top) * p.c);
+                    f1 = ml1.x == -INFINITY ? 0.0f : exp2_approx((ml1.x - top) * p.c);
+                    l = l * f0 + ml1.y * f1;
+                    m = top;
+                }
+                tc_fence_after();
+                if (item.slot < 0) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    f0 *= inv;
+                    f1 *= inv;
+                }
+                const bool poisoned = *static_cast<volatile int *>(&sm.poison_piece) == it;
+                __nv_bfloat16 *dst = p.out + int64_t(item.q_row + tt) * p.o_row + int64_t(item.kvh * p.G + g) * p.o_head;
+                const int64_t prow = int64_t(item.slot) * (PAIR ? 2 * kRows : kRows) + s * kRows + r;
+                if (item.slot >= 0 && mine)
+                    p.part_ml[prow] = make_float2(m, l);
+                if (nb || item.slot < 0) {
+#pragma unroll 1
+                    for (int x = 0; x < kHD; x += 32) {
+                        uint32_t o[32];
+                        if (nb) {
+                            tmem_ld32_wait(o_tmem + uint32_t(x), o);
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                o[y] = 0u;
+                        }
+                        float a[32];
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            a[y] = __uint_as_float(o[y]) * f0;
+                        if (second) {
+                            tmem_ld32_wait(o_tmem + uint32_t(kHD + x), o);
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                a[y] = fmaf(__uint_as_float(o[y]), f1, a[y]);
+                        }
+                        if (poisoned) {
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                if (limit > sm.poison[x + y])
+                                    a[y] = __uint_as_float(0x7fffffffu);
+                        }
+                        if (!mine)
+                            continue;
+                        if (item.slot < 0) {
+#pragma unroll
+                            for (int y = 0; y < 32; y += 8)
+                                *reinterpret_cast<uint4 *>(dst + x + y) =
+                                    make_uint4(bf16x2(a[y], a[y + 1]), bf16x2(a[y + 2], a[y + 3]),
+                                               bf16x2(a[y + 4], a[y + 5]), bf16x2(a[y + 6], a[y + 7]));
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < 32; y += 4)
+                                *reinterpret_cast<float4 *>(p.part_o + prow * kHD + x + y) =
+                                    make_float4(a[y], a[y + 1], a[y + 2], a[y + 3]);
+                        }
+                    }
+                }
+                if (!PAIR && second) {
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sm.o1_read));
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&sm.item_empty[islot]));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- joining the parts of cut tiles
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSplit = 4;        // CTAs per cut tile
+
+// CTA (c, y) takes every kJoinSplit-th row of the tile whose first part CTA c
+// of the main kernel holds.  `span` warps share a row's parts (as many as
+// there are parts, up to all of them), each adding its own in order, then the
+// warps' sums are added in order.
+template <bool PAIR>
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const PrefillParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kWarps = kJoinThreads / 32;
+    __shared__ float4 acc_s[kWarps][32];
+    __shared__ float l_s[kWarps], m_s[kWarps];
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (!ld_dep_u32(&p.hdr[c].valid))
+        return;
+    const JoinHeader h{1, int(ld_dep_u32(&p.hdr[c].kvh)), int(ld_dep_u32(&p.hdr[c].q_row)),
+                       int(ld_dep_u32(&p.hdr[c].toks)), int(ld_dep_u32(&p.hdr[c].last)), {}};
+    const int parts = h.last - c + 1;
+    int span = 1;
+    while (span < parts && span < kWarps)
+        span *= 2;
+    constexpr int64_t kSlotRows = PAIR ? 2 * kRows : kRows;
+    const int rows = h.toks * p.G, team = warp / span, in = warp % span;
+    auto slot_of = [&](int i) { return int64_t(i ? 2 * (c + i) : 2 * c + 1); };
+    for (int base = blockIdx.y * (kWarps / span); base < rows; base += kJoinSplit * (kWarps / span)) {
+        const int row = base + team;                        // token * G + head of the group
+        const bool here = row < rows;
+        const int tok = row / p.G, g = row - tok * p.G;
+        const int tile = PAIR ? tok / p.TM : 0;             // stream
+        const int64_t at = tile * kRows + (tok - tile * p.TM) * p.G + g;
+        float m = -INFINITY, l = 0.0f;
+        float4 acc = {};
+        if (here) {
+            for (int i = in; i < parts; i += span)
+                m = fmaxf(m, __ldcg(&p.part_ml[slot_of(i) * kSlotRows + at]).x);
+#pragma unroll 4
+            for (int i = in; i < parts; i += span) {
+                const int64_t pr = slot_of(i) * kSlotRows + at;
+                const float2 ml = __ldcg(&p.part_ml[pr]);
+                if (ml.x == -INFINITY && ml.y == 0.0f)
+                    continue;                               // no visible key in this part
+                const float f = exp2f((ml.x - m) * p.c);
+                const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * kHD) + lane);
+                l = fmaf(ml.y, f, l);
+                acc.x = fmaf(o.x, f, acc.x);
+                acc.y = fmaf(o.y, f, acc.y);
+                acc.z = fmaf(o.z, f, acc.z);
+                acc.w = fmaf(o.w, f, acc.w);
+            }
+        }
+        acc_s[warp][lane] = acc;
+        if (lane == 0) {
+            l_s[warp] = l;
+            m_s[warp] = m;
+        }
+        __syncthreads();
+        if (here && in == 0) {
+            for (int i = 1; i < span; ++i)
+                m = fmaxf(m, m_s[warp + i]);
+            l = 0.0f;
+            acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int i = 0; i < span; ++i) {
+                const float mi = m_s[warp + i];
+                const float f = mi == -INFINITY ? 0.0f : exp2f((mi - m) * p.c);
+                const float4 o = acc_s[warp + i][lane];
+                if (mi == -INFINITY && l_s[warp + i] == 0.0f)
+                    continue;
+                l = fmaf(l_s[warp + i], f, l);
+                acc.x = fmaf(o.x, f, acc.x);
+                acc.y = fmaf(o.y, f, acc.y);
+                acc.z = fmaf(o.z, f, acc.z);
+                acc.w = fmaf(o.w, f, acc.w);
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            __nv_bfloat16 *dst = p.out + int64_t(h.q_row + tok) * p.o_row + int64_t(h.kvh * p.G + g) * p.o_head;
+            *reinterpret_cast<uint2 *>(dst + 4 * lane) =
+                make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            ptr = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// [rows][heads][128] bf16 as a 3-D map, boxes of 64 values x box_heads x box_rows.
+int make_map(CUtensorMap *map, const bitlinear_heads &h, int heads, uint32_t box_heads, uint32_t box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn)
+        return BL_ERR_CUDA;
+    const cuuint64_t dims[3] = {kHD, cuuint64_t(heads), cuuint64_t(h.rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(heads == 1 ? kHD : h.head_stride) * 2,
+                                   cuuint64_t(h.rows == 1 ? kHD : h.row_stride) * 2};
+    const cuuint32_t box[3] = {64, box_heads, box_rows}, estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, h.data, dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? BL_OK : BL_ERR_CUDA;
+}
+
+// Workspace: a join header per CTA, then the parts' m and l, then their O.
+struct WsLayout {
+    size_t ml, o, total;
+};
+
+WsLayout ws_layout(int grid)
+{
+    WsLayout w{};
+    w.ml = (size_t(grid) * sizeof(JoinHeader) + 127) / 128 * 128;
+    w.o = w.ml + size_t(grid) * 2 * (2 * kRows) * sizeof(float2);
+    w.total = w.o + size_t(grid) * 2 * (2 * kRows) * kHD * sizeof(float);
+    return w;
+}
+
+template <bool PAIR>
+int launch_mode(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const PrefillParams &p, int grid,
+                unsigned flags, cudaStream_t s)
+{
+    int per_sm = 0;
+    int st = occupancy(reinterpret_cast<const void *>(prefill_kernel<PAIR>), kThreads, smem_bytes<PAIR>(), &per_sm);
+    if (st)
+        return st;
+    if (per_sm < 1)
+        return BL_ERR_UNSUPPORTED;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<PAIR>();
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = flags & BL_FLAG_PDL ? 1 : 0;
+    if ((st = cuda_status(cudaLaunchKernelEx(&cfg, prefill_kernel<PAIR>, qm, km, vm, p))))
+        return st;
+    cfg.gridDim = dim3(unsigned(grid), kJoinSplit);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;       // it waits for the main kernel's results itself
+    return cuda_status(cudaLaunchKernelEx(&cfg, prefill_join_kernel<PAIR>, p));
 }
 
 }  // namespace
 
-size_t attention_prefill_workspace_bytes(int, int) { return 16; }
+size_t attention_prefill_workspace_bytes(int, int)
+{
+    const DeviceInfo *di = device_info();
+    return di ? ws_layout(di->sm_count).total : 0;
+}
 
 int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s)
 {
     const DeviceInfo *di = device_info();
     if (!di)
         return BL_ERR_CUDA;
-    const PrefillParams p{static_cast<const __nv_bfloat16 *>(a.q.data), static_cast<const __nv_bfloat16 *>(a.k.data),
-                          static_cast<const __nv_bfloat16 *>(a.v.data), static_cast<__nv_bfloat16 *>(a.out.data),
-                          a.q.row_stride, a.q.head_stride, a.k.row_stride, a.k.head_stride, a.v.row_stride,
-                          a.v.head_stride, a.out.row_stride, a.out.head_stride, a.cu_q, a.cu_k, a.batch, a.H,
-                          a.H / a.Hkv, a.q.rows, a.k.rows, a.scale, di->status};
-    const int64_t blocks = (p.Tq * p.H + 3) / 4;
-    if (blocks > 0x7fffffff)
-        return BL_ERR_SHAPE;
-    prefill_kernel<<<unsigned(blocks), 128, 0, s>>>(p);
-    return launch_status();
+    const int grid = di->sm_count, G = a.H / a.Hkv;
+    const WsLayout w = ws_layout(grid);
+    auto *base = static_cast<unsigned char *>(a.ws);
+    PrefillParams p{};
+    p.out = static_cast<__nv_bfloat16 *>(a.out.data);
+    p.o_row = a.out.row_stride;
+    p.o_head = a.out.head_stride;
+    p.cu_q = a.cu_q;
+    p.cu_k = a.cu_k;
+    p.batch = a.batch;
+    p.Hkv = a.Hkv;
+    p.G = G;
+    p.TM = kRows / G;
+    p.Tq = a.q.rows;
+    p.Tk = a.k.rows;
+    p.c = a.scale * 1.44269504088896340736f;
+    p.hdr = reinterpret_cast<JoinHeader *>(base);
+    p.part_ml = reinterpret_cast<float2 *>(base + w.ml);
+    p.part_o = reinterpret_cast<float *>(base + w.o);
+    p.status = di->status;
+    CUtensorMap qm, km, vm;
+    int st;
+    if ((st = make_map(&qm, a.q, a.H, uint32_t(G), uint32_t(p.TM))) ||
+        (st = make_map(&km, a.k, a.Hkv, 1, kKeys)) || (st = make_map(&vm, a.v, a.Hkv, 1, kKeys)))
+        return st;
+    // two tiles of rows per CTA once every CTA could have a pair of them
+    const int64_t pairs = int64_t(a.Hkv) * (p.Tq / (2 * p.TM));
+    return pairs >= grid / 4 ? launch_mode<true>(qm, km, vm, p, grid, a.flags, s)
+                             : launch_mode<false>(qm, km, vm, p, grid, a.flags, s);
 }
 
 }  // namespace bl
