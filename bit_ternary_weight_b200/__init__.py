@@ -144,7 +144,7 @@ class HeadsC(ctypes.Structure):
                 ("head_stride", ctypes.c_int64)]
 
 
-_heads_p = ctypes.POINTER(HeadsC)
+_heads_p = _vp   # the address of a HeadsC or of four int64 laid out like it
 _SIGNATURES.update({
     "bitlinear_qk_norm_rope": (_int, [_heads_p, _heads_p, _heads_p, _int, _int, _int, _int, _vp,
                                       _vp, _i64, _vp, _vp, _int, ctypes.c_float, _vp, _heads_p,
@@ -184,6 +184,9 @@ def _ptr(t):
 
 
 def _stream(device: torch.device):
+    if device.type == "cuda" and device.index is not None:
+        # the current stream's handle without a Stream object around it
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
     # a CPU tensor still goes to the library, which rejects host pointers
     dev = device if device.type == "cuda" else None
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
@@ -195,6 +198,19 @@ def _on(device: torch.device):
     if device.type == "cuda":
         return torch.cuda.device(device)
     return contextlib.nullcontext()
+
+
+def _call(fn, where: str, device: torch.device, args):
+    """fn(*args, stream) on the tensors' GPU and its current stream.  Entering a
+    device costs more host time than the rest of a short call, so it is done
+    only where another one is current."""
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device))
+    else:
+        status = fn(*args, _stream(device))
+    if status != BL_OK:
+        raise BitLinearError(status, where)
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
@@ -657,26 +673,43 @@ def position_advance(pos: torch.Tensor):
 BL_FLAG_ROPE_HALVES = 8
 
 
-def _heads(t, where: str, name: str, dtypes, heads: int | None = None, rows: int | None = None):
-    """The rows of heads [rows][heads][128] of a tensor, any strides above the
-    contiguous 128 values of a head."""
+def _scratch(size, where: str, device: torch.device, *args) -> torch.Tensor:
+    """Device memory of the bytes that the library's `size` function says."""
+    if device.type == "cuda" and device.index not in (None, torch.cuda.current_device()):
+        with torch.cuda.device(device):
+            n = size(*args)
+    else:
+        n = size(*args)
+    if not n:
+        raise BitLinearError(BL_ERR_SHAPE, where)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _heads(t, where: str, name: str, dtypes, heads, rows):
+    """The rows of heads [rows][heads][128] of a tensor (None: any number), as
+    the four numbers of a HeadsC."""
+    shape, stride = t.shape, t.stride()
     if t.dtype not in dtypes:
         want = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise BitLinearError(BL_ERR_DTYPE, where,
                              f"{name} is {str(t.dtype).replace('torch.', '')}, needs {want}")
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != 128 or t.stride(2) != 1 or shape[0] < 1 or shape[1] < 1 or \
+    if len(shape) != 3 or shape[2] != 128 or stride[2] != 1 or \
             (heads is not None and shape[1] != heads) or (rows is not None and shape[0] != rows):
         raise BitLinearError(
-            BL_ERR_SHAPE, where, f"{name} of shape {tuple(shape)} and strides {tuple(t.stride())} is not "
+            BL_ERR_SHAPE, where, f"{name} of shape {tuple(shape)} and strides {stride} is not "
             f"[{'rows' if rows is None else rows}][{'heads' if heads is None else heads}][128]")
-    return HeadsC(t.data_ptr(), shape[0], t.stride(0), t.stride(1))
+    return t.data_ptr(), shape[0], stride[0], stride[1]
+
+
+_HeadsArray = {n: ctypes.c_int64 * (4 * n) for n in (4, 6)}
+_NO_HEADS = (0, 0, 0, 0)
 
 
 def _vector(t, where: str, name: str, dtypes, n: int):
-    """A contiguous vector (or array) of at least n elements."""
+    """The address of a contiguous vector (or array) of at least n elements."""
     if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < n:
         _fits(t, where, name, dtypes, 1, n)
+    return t.data_ptr()
 
 
 def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float = RMS_EPS,
@@ -699,55 +732,53 @@ def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float
     where = "bitlinear_qk_norm_rope"
     if q.dim() != 3 or k.dim() != 3:
         raise BitLinearError(BL_ERR_SHAPE, where, f"q of shape {tuple(q.shape)}, k of shape {tuple(k.shape)}")
-    T, H, Hkv = q.shape[0], q.shape[1], k.shape[1]
-    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+    T, H, _ = q.shape
+    Hkv = k.shape[1]
+    dtype, device = q.dtype, q.device
+    if k.dtype != dtype or (v is not None and v.dtype != dtype):
         raise BitLinearError(BL_ERR_DTYPE, where, "q, k and v of mixed element types")
     if (v is None and v_out is not None) or (slots is not None and (
             k_out is None or (v is not None and v_out is None))):
         raise BitLinearError(BL_ERR_NULL, where, "slots need k_out and v_out, v_out needs v")
     if q_out is None:
-        q_out = torch.empty(T, H, 128, dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty(T, H, 128, dtype=torch.bfloat16, device=device)
     if k_out is None:
-        k_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=q.device)
+        k_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=device)
     if v is not None and v_out is None:
-        v_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=q.device)
-    qh, kh = _heads(q, where, "q", _FLOATS), _heads(k, where, "k", _FLOATS, Hkv, T)
-    vh = None if v is None else _heads(v, where, "v", _FLOATS, Hkv, T)
-    qo, ko = _heads(q_out, where, "q_out", _BF16, H, T), _heads(k_out, where, "k_out", _BF16, Hkv)
-    vo = None if v is None else _heads(v_out, where, "v_out", _BF16, Hkv, ko.rows)
-    if slots is None and ko.rows < T:
-        raise BitLinearError(BL_ERR_SHAPE, where, f"k_out has {ko.rows} rows for {T} tokens")
-    _vector(positions, where, "positions", _I32, T)
-    if table.dim() != 3 or table.shape[1] != 64 or table.shape[2] != 2:
-        raise BitLinearError(BL_ERR_SHAPE, where, f"table of shape {tuple(table.shape)} is not [positions][64][2]")
-    _vector(table, where, "table", _F32, table.shape[0] * 128)
+        v_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=device)
+    ko = _heads(k_out, where, "k_out", _BF16, Hkv, None)
+    arr = _HeadsArray[6](
+        *_heads(q, where, "q", _FLOATS, H, T), *_heads(k, where, "k", _FLOATS, Hkv, T),
+        *(_NO_HEADS if v is None else _heads(v, where, "v", _FLOATS, Hkv, T)),
+        *_heads(q_out, where, "q_out", _BF16, H, T), *ko,
+        *(_NO_HEADS if v is None else _heads(v_out, where, "v_out", _BF16, Hkv, ko[1])))
+    if slots is None and ko[1] < T:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"k_out has {ko[1]} rows for {T} tokens")
+    rows = table.shape
+    if len(rows) != 3 or rows[1] != 64 or rows[2] != 2:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"table of shape {tuple(rows)} is not [positions][64][2]")
     gt = BL_F32
-    for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+    gains = [None, None]
+    for i, g in enumerate((q_gain, k_gain)):
         if g is not None:
-            _vector(g, where, name, _FLOATS, 128)
+            gains[i] = _vector(g, where, "k_gain" if i else "q_gain", _FLOATS, 128)
             gt = _dt(g.dtype)
     if q_gain is not None and k_gain is not None and q_gain.dtype != k_gain.dtype:
         raise BitLinearError(BL_ERR_DTYPE, where, "gains of mixed element types")
-    if slots is not None:
-        _vector(slots, where, "slots", _I32, T)
+    at = ctypes.addressof(arr)
     flags = (BL_FLAG_PDL if pdl else 0) | (BL_FLAG_ROPE_HALVES if halves else 0)
-    with _on(q.device):
-        _check(_lib.bitlinear_qk_norm_rope(qh, kh, vh, _dt(q.dtype), H, Hkv, 128, _ptr(positions),
-                                           _ptr(table), table.shape[0], _ptr(q_gain), _ptr(k_gain), gt,
-                                           float(eps), _ptr(slots), qo, ko, vo, flags,
-                                           _stream(q.device)), where)
+    _call(_lib.bitlinear_qk_norm_rope, where, device, (
+        at, at + 32, at + 64, _dt(dtype), H, Hkv, 128, _vector(positions, where, "positions", _I32, T),
+        _vector(table, where, "table", _F32, rows[0] * 128), rows[0], gains[0], gains[1], gt, eps,
+        None if slots is None else _vector(slots, where, "slots", _I32, T), at + 96, at + 128, at + 160, flags))
     return q_out, k_out, v_out
 
 
 def attention_prefill_workspace(H: int, Hkv: int, device) -> torch.Tensor:
     """A workspace for attention_prefill of any lengths (reusable by ordered
     calls; its contents do not matter)."""
-    dev = torch.device(device)
-    with _on(dev):
-        n = int(_lib.bitlinear_attention_prefill_workspace_bytes(H, Hkv))
-    if n == 0:
-        raise BitLinearError(BL_ERR_SHAPE, "bitlinear_attention_prefill_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=dev)
+    return _scratch(_lib.bitlinear_attention_prefill_workspace_bytes, "bitlinear_attention_prefill_workspace_bytes",
+                    torch.device(device), H, Hkv)
 
 
 def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=None,
@@ -767,41 +798,48 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=
     where = "bitlinear_attention_prefill"
     if q.dim() != 3 or k.dim() != 3:
         raise BitLinearError(BL_ERR_SHAPE, where, f"q of shape {tuple(q.shape)}, k of shape {tuple(k.shape)}")
+    device = q.device
     if cu_k is None:
         cu_k = cu_q
     if out is None:
-        out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
-    T, H, Hkv = q.shape[0], q.shape[1], k.shape[1]
+        out = torch.zeros(q.shape, dtype=torch.bfloat16, device=device)
+    T, H, _ = q.shape
+    Hkv = k.shape[1]
     if Hkv < 1 or H % Hkv:
         raise BitLinearError(BL_ERR_SHAPE, where, f"{H} query heads for {Hkv} kv heads")
-    qh, kh = _heads(q, where, "q", _BF16), _heads(k, where, "k", _BF16)
-    vh, oh = _heads(v, where, "v", _BF16, Hkv, kh.rows), _heads(out, where, "out", _BF16, H, T)
     batch = cu_q.numel() - 1
-    _vector(cu_q, where, "cu_q", _I32, 2)
-    _vector(cu_k, where, "cu_k", _I32, 2)
+    bounds = _vector(cu_q, where, "cu_q", _I32, 2), _vector(cu_k, where, "cu_k", _I32, 2)
     if cu_k.numel() != batch + 1:
         raise BitLinearError(BL_ERR_SHAPE, where, f"cu_q of {batch + 1} bounds, cu_k of {cu_k.numel()}")
+    kh = _heads(k, where, "k", _BF16, None, None)
+    arr = _HeadsArray[4](*_heads(q, where, "q", _BF16, None, None), *kh, *_heads(v, where, "v", _BF16, Hkv, kh[1]),
+                         *_heads(out, where, "out", _BF16, H, T))
     if workspace is None:
-        workspace = attention_prefill_workspace(H, Hkv, q.device)
-    _vector(workspace, where, "workspace", (workspace.dtype,), 1)
-    with _on(q.device):
-        _check(_lib.bitlinear_attention_prefill(
-            qh, kh, vh, _ptr(cu_q), _ptr(cu_k), batch, H, Hkv, 128,
-            128 ** -0.5 if scale is None else float(scale), oh, _ptr(workspace),
-            workspace.numel() * workspace.element_size(), BL_FLAG_PDL if pdl else 0,
-            _stream(q.device)), where)
+        workspace = attention_prefill_workspace(H, Hkv, device)
+    ws = _vector(workspace, where, "workspace", (workspace.dtype,), 1)
+    at = ctypes.addressof(arr)
+    _call(_lib.bitlinear_attention_prefill, where, device, (
+        at, at + 32, at + 64, *bounds, batch, H, Hkv, 128, 128 ** -0.5 if scale is None else scale, at + 96, ws,
+        workspace.nbytes, BL_FLAG_PDL if pdl else 0))
     return out
 
 
 def adapter_workspace(T: int, r: int, device) -> torch.Tensor:
     """A workspace for adapter_add of up to T tokens and rank r (reusable by
     ordered calls; its contents do not matter)."""
-    dev = torch.device(device)
-    with _on(dev):
-        n = int(_lib.bitlinear_adapter_workspace_bytes(T, r))
-    if n == 0:
-        raise BitLinearError(BL_ERR_SHAPE, "bitlinear_adapter_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=dev)
+    return _scratch(_lib.bitlinear_adapter_workspace_bytes, "bitlinear_adapter_workspace_bytes",
+                    torch.device(device), T, r)
+
+
+def _rows(t, where: str, name: str, dtypes, rows: int, cols: int) -> int:
+    """The row pitch of a tensor [rows, cols] whose rows are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype not in dtypes or len(shape) != 2 or shape[0] != rows or shape[1] != cols or \
+            (stride[1] != 1 and cols > 1) or (stride[0] < cols and rows > 1):
+        _fits(t, where, name, dtypes, rows, cols, max(cols, stride[0]))
+        raise BitLinearError(BL_ERR_SHAPE, where,
+                             f"{name} of shape {tuple(shape)} and strides {stride} is not [{rows}][{cols}]")
+    return stride[0] if rows > 1 else cols
 
 
 def adapter_add(y, x, down, up, index, scale=None, out=None, workspace=None, pdl: bool = False):
@@ -818,31 +856,24 @@ def adapter_add(y, x, down, up, index, scale=None, out=None, workspace=None, pdl
     where = "bitlinear_adapter_add"
     if y.dim() != 2 or x.dim() != 2 or down.dim() != 3 or up.dim() != 3:
         raise BitLinearError(BL_ERR_SHAPE, where, "y and x have two dimensions, down and up three")
-    (T, N), K, (n, r) = y.shape, x.shape[1], down.shape[:2]
-    if tuple(down.shape) != (n, r, K) or tuple(up.shape) != (n, N, r):
+    (T, N), K, (n, r, dk) = y.shape, x.shape[1], down.shape
+    if dk != K or tuple(up.shape) != (n, N, r):
         raise BitLinearError(BL_ERR_SHAPE, where, f"down of shape {tuple(down.shape)} and up of shape "
                              f"{tuple(up.shape)} for K={K}, N={N}")
+    device = y.device
     if out is None:
-        out = torch.empty(T, N, dtype=y.dtype, device=y.device)
+        out = torch.empty(T, N, dtype=y.dtype, device=device)
     if out.dtype != y.dtype:
         raise BitLinearError(BL_ERR_DTYPE, where, "out and y of different element types")
-    ldy, ldx, ldo = (t.stride(0) if T > 1 else t.shape[1] for t in (y, x, out))
-    _fits(y, where, "y", _FLOATS, T, N, ldy)
-    _fits(x, where, "x", _BF16, T, K, ldx)
-    _fits(out, where, "out", _FLOATS, T, N, ldo)
-    _vector(down, where, "down", _BF16, n * r * K)
-    _vector(up, where, "up", _BF16, n * N * r)
-    _vector(index, where, "index", _I32, T)
-    if scale is not None:
-        _vector(scale, where, "scale", _F32, n)
+    ldy, ldx = _rows(y, where, "y", _FLOATS, T, N), _rows(x, where, "x", _BF16, T, K)
+    ldo = _rows(out, where, "out", _FLOATS, T, N)
     if workspace is None:
-        workspace = adapter_workspace(T, r, y.device)
-    _vector(workspace, where, "workspace", (workspace.dtype,), 1)
-    with _on(y.device):
-        _check(_lib.bitlinear_adapter_add(
-            _ptr(y), _dt(y.dtype), ldy, _ptr(x), ldx, T, N, K, _ptr(down), _ptr(up), n, r, _ptr(index),
-            _ptr(scale), _ptr(out), ldo, _ptr(workspace), workspace.numel() * workspace.element_size(),
-            BL_FLAG_PDL if pdl else 0, _stream(y.device)), where)
+        workspace = adapter_workspace(T, r, device)
+    _call(_lib.bitlinear_adapter_add, where, device, (
+        y.data_ptr(), _dt(y.dtype), ldy, x.data_ptr(), ldx, T, N, K, _vector(down, where, "down", _BF16, n * r * K),
+        _vector(up, where, "up", _BF16, n * N * r), n, r, _vector(index, where, "index", _I32, T),
+        None if scale is None else _vector(scale, where, "scale", _F32, n), out.data_ptr(), ldo,
+        _vector(workspace, where, "workspace", (workspace.dtype,), 1), workspace.nbytes, BL_FLAG_PDL if pdl else 0))
     return out
 
 

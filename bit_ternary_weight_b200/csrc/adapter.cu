@@ -1,77 +1,442 @@
-// adapter.cu -- low-rank adapters of many requests beside one projection:
-//   u[t] = down[a] x[t] (fp32, workspace), out[t] = y[t] + scale[a] up[a] u[t].
-// One warp per (token, rank) of u, one thread per output.
+// adapter.cu -- low-rank adapters of many requests beside one shared
+// projection: out[t] = y[t] + scale[a] up[a] (down[a] x[t]), a = index[t].
+//
+// Two launches, the second chained to the first (programmatic dependent
+// launch): u[t] = scale[a] down[a] x[t] in fp32 to the workspace, then
+// out = y + up u.  Both are bound by memory: a token brings 2 r (K + N)
+// multiply-adds against 2 K + 4 N bytes, and a few tokens bring their whole
+// adapters, so the products run as mma.sync m16n8k16 straight from registers
+// (r columns or r terms are far too few for a tcgen05 tile) and the work is
+// in keeping loads in flight:
+//   - a tile is 16 tokens; the tokens' distinct adapters are found with one
+//     match across the warp and taken one after the other, each giving only
+//     its own tokens' rows (the other rows of its products are dropped, so
+//     nothing of an adapter reaches a token that does not use it);
+//   - a sum does not mind the order of its terms, so the k index of an MMA is
+//     permuted such that each lane's operands are contiguous: 16 bytes of x
+//     and of down (8 consecutive k of a 32-k group, two MMAs), 8 bytes of up
+//     (4 consecutive ranks); the same for the output columns (four n8 tiles
+//     interleaved give a lane 8 consecutive columns of y and out).
+// With few tokens the adapters of a tile go to different CTAs (first launch)
+// or warps (second), and K is split over CTAs whose partial sums the second
+// launch adds in order: the same call gives the same bits.
+// u enters the second product as a sum of bf16 values, each the rest of the
+// one before: two (16 bits of it) for bf16 outputs, three (24 bits) for fp32
+// outputs; one alone would cost an output 2^-8 of the adapter's share.
+#include <algorithm>
+
 #include "bl_common.cuh"
 
 namespace bl {
 namespace {
 
-__global__ void __launch_bounds__(128) adapter_down_kernel(const AdapterArgs a, float *u, int *status)
+constexpr int kTile = 16;                 // tokens per tile (MMA M)
+constexpr int kDownWarps = 8, kUpWarps = 8;
+constexpr int kUpCols = 32;               // output columns per warp
+constexpr int kUpTokens = 64;             // tokens per CTA of the second launch (many tokens)
+
+struct AdapterParams {
+    const void *y;
+    int64_t ldy;
+    const __nv_bfloat16 *x;
+    int64_t ldx, T, N, K;
+    const __nv_bfloat16 *down, *up;
+    int n, r;
+    const int32_t *index;
+    const float *scale;
+    void *out;
+    int64_t ldo;
+    float *u;                             // [splits][T][r]
+    int splits;
+    int down_ways;                        // CTAs that share the adapters of a tile
+    int vec;                              // y and out rows take 16-byte vectors
+    int *status;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
 {
-    const int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int64_t t = item / a.r;
-    const int j = int(item - t * a.r);
-    if (t >= a.T)
-        return;
-    const int id = a.index[t];
-    if (id < 0)
-        return;
-    if (id >= a.n) {
-        if (lane == 0)
-            atomicExch(status, BL_ERR_SHAPE);
-        return;
-    }
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x) + t * a.ldx;
-    const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(a.down) + (int64_t(id) * a.r + j) * a.K;
-    float s = 0.0f;
-    for (int64_t k = lane; k < a.K; k += 32)
-        s = fmaf(__bfloat162float(x[k]), __bfloat162float(w[k]), s);
-    s = warp_sum(s);
-    if (lane == 0)
-        u[t * a.r + j] = a.scale ? s * a.scale[id] : s;
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__global__ void __launch_bounds__(128) adapter_up_kernel(const AdapterArgs a, const float *u)
+// The adapter of token t0 + lane (lanes 0 .. 15), -1: none; an id that does
+// not exist counts as none.
+__device__ __forceinline__ int tile_id(const AdapterParams &p, int64_t t0, int lane, bool report)
 {
-    const int64_t n = int64_t(blockIdx.x) * 128 + threadIdx.x;
-    if (n >= a.N)
-        return;
-    for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
-        const int id = a.index[t];
-        float v = a.yt == BL_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.y)[t * a.ldy + n])
-                                  : static_cast<const float *>(a.y)[t * a.ldy + n];
-        if (id >= 0 && id < a.n) {
-            const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(a.up) + (int64_t(id) * a.N + n) * a.r;
-            float s = 0.0f;
-            for (int j = 0; j < a.r; ++j)
-                s = fmaf(u[t * a.r + j], __bfloat162float(w[j]), s);
-            v += s;
-        }
-        store_y(a.out, a.yt, t * a.ldo + n, v);
+    int id = -1;
+    if (lane < kTile && t0 + lane < p.T)
+        id = int(ld_dep_u32(p.index + t0 + lane));
+    if (id >= p.n) {
+        if (report)
+            atomicExch(p.status, BL_ERR_SHAPE);
+        id = -1;
     }
+    return id < 0 ? -1 : id;
+}
+
+// Lanes that are the first with their adapter.
+__device__ __forceinline__ unsigned first_of(int id, int lane)
+{
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    return __ballot_sync(0xffffffffu, id >= 0 && lane == __ffs(same) - 1);
+}
+
+// u of one tile, one K split: the warps take the split's 32-k groups in turn
+// and their sums are added through shared memory in a fixed order.
+template <int NT>
+__global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const AdapterParams p)
+{
+    __shared__ float red[kDownWarps / 2][kTile][NT * 8];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int64_t t0 = int64_t(blockIdx.x) * kTile;
+    const int way = blockIdx.y, split = blockIdx.z;
+    const int id = tile_id(p, t0, lane, way == 0 && split == 0);
+    unsigned firsts = first_of(id, lane);
+    const int groups = int(p.K / 32);
+    const int k0 = int(int64_t(split) * groups / p.splits), k1 = int(int64_t(split + 1) * groups / p.splits);
+    for (int ord = 0; firsts; ++ord, firsts &= firsts - 1) {
+        if (ord % p.down_ways != way)
+            continue;
+        const int a = __shfl_sync(0xffffffffu, id, __ffs(firsts) - 1);
+        const unsigned rows = __ballot_sync(0xffffffffu, id == a);
+        const bool r0 = rows >> g & 1, r1 = rows >> (g + 8) & 1;
+        const __nv_bfloat16 *x0 = p.x + (t0 + g) * p.ldx + 8 * c, *x1 = x0 + 8 * p.ldx;
+        const __nv_bfloat16 *w = p.down + (int64_t(a) * p.r + g) * p.K + 8 * c;
+        float acc[NT][4] = {};
+        auto step = [&](const uint4 &xa, const uint4 &xb, const uint4 (&b)[NT]) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mma_bf16(acc[j], xa.x, xb.x, xa.y, xb.y, b[j].x, b[j].y);
+                mma_bf16(acc[j], xa.z, xb.z, xa.w, xb.w, b[j].z, b[j].w);
+            }
+        };
+        constexpr int kDeep = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;      // groups in flight
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        int k = k0 + warp;
+        for (; k + (kDeep - 1) * kDownWarps < k1; k += kDeep * kDownWarps) {
+            uint4 xa[kDeep], xb[kDeep], b[kDeep][NT];
+#pragma unroll
+            for (int s = 0; s < kDeep; ++s) {
+                const int64_t at = int64_t(k + s * kDownWarps) * 32;
+                xa[s] = r0 ? ld_dep_v4(x0 + at) : zero;
+                xb[s] = r1 ? ld_dep_v4(x1 + at) : zero;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    b[s][j] = j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
+            }
+#pragma unroll
+            for (int s = 0; s < kDeep; ++s)
+                step(xa[s], xb[s], b[s]);
+        }
+        for (; k < k1; k += kDownWarps) {
+            uint4 b[NT];
+            const int64_t at = int64_t(k) * 32;
+            const uint4 xa = r0 ? ld_dep_v4(x0 + at) : zero, xb = r1 ? ld_dep_v4(x1 + at) : zero;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                b[j] = j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
+            step(xa, xb, b);
+        }
+        // sums of warps w and w + 4, then of the four pairs
+        const int pair = warp & (kDownWarps / 2 - 1);
+        for (int half = 1; half >= 0; --half) {
+            if (warp / (kDownWarps / 2) == half) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float &s = red[pair][g + 8 * (e >> 1)][8 * j + 2 * c + (e & 1)];
+                        s = half ? acc[j][e] : s + acc[j][e];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        const float scale = p.scale ? __ldcg(p.scale + a) : 1.0f;
+        for (int e = threadIdx.x; e < kTile * p.r; e += kDownWarps * 32) {
+            const int row = e / p.r, j = e - row * p.r;
+            if (rows >> row & 1) {
+                float s = red[0][row][j];
+#pragma unroll
+                for (int q = 1; q < kDownWarps / 2; ++q)
+                    s += red[q][row][j];
+                __stcg(p.u + (int64_t(split) * p.T + t0 + row) * p.r + j, s * scale);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Eight consecutive columns n .. n + 7 of row t.
+template <bool F32>
+__device__ __forceinline__ void load_cols(const AdapterParams &p, int64_t t, int64_t n, float (&f)[8])
+{
+    const int64_t at = t * p.ldy + n;
+    if (p.vec && n + 8 <= p.N) {
+        load8<F32 ? BL_F32 : BL_BF16, true>(p.y, at, f);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (n + i >= p.N)
+            f[i] = 0.0f;
+        else if (F32)
+            f[i] = __uint_as_float(ld_dep_u32(static_cast<const float *>(p.y) + at + i));
+        else
+            f[i] = __uint_as_float(ld_dep_u16(static_cast<const __nv_bfloat16 *>(p.y) + at + i) << 16);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store_cols(const AdapterParams &p, int64_t t, int64_t n, const float (&f)[8])
+{
+    const int64_t at = t * p.ldo + n;
+    if (p.vec && n + 8 <= p.N) {
+        if (F32) {
+            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (n + i < p.N)
+            store_y(p.out, F32 ? BL_F32 : BL_BF16, at + i, f[i]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// The values (a, b) as sums of TERMS bf16 values, largest first.
+template <int TERMS>
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[TERMS])
+{
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        w[i] = pack_bf16(a, b);
+        a -= __uint_as_float(w[i] << 16);
+        b -= __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// out = y + up u.  A warp has 32 columns; WAYS = 1: the warps of a CTA lie side
+// by side and walk its 64 tokens; WAYS = 8: they share the columns and the 16
+// tokens' adapters.
+template <int KB, bool F32, int WAYS>
+__global__ void __launch_bounds__(kUpWarps * 32, KB <= 2 ? 3 : 2) adapter_up_kernel(const AdapterParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int way = WAYS == 1 ? 0 : warp;
+    const int64_t n0 = (int64_t(blockIdx.x) * (kUpWarps / WAYS) + (WAYS == 1 ? warp : 0)) * kUpCols;
+    if (n0 >= p.N)
+        return;
+    const int64_t nc = n0 + 8 * c;                            // this lane's output columns
+    constexpr int kTokens = WAYS == 1 ? kUpTokens : kTile;
+    const int64_t tiles = (p.T + kTile - 1) / kTile;
+    // this CTA's tiles: runs of kTokens / kTile, gridDim.y runs apart
+    for (int64_t i = 0;; ++i) {
+        const int64_t tile = (int64_t(blockIdx.y) + i / (kTokens / kTile) * gridDim.y) * (kTokens / kTile) +
+                             i % (kTokens / kTile);
+        if (tile >= tiles)
+            break;
+        const int64_t t0 = tile * kTile;
+        const int id = tile_id(p, t0, lane, false);
+        unsigned firsts = first_of(id, lane);
+        const unsigned none = __ballot_sync(0xffffffffu, lane < kTile && t0 + lane < p.T && id < 0);
+        float y[2][8];
+        const int64_t ta = t0 + g, tb = ta + 8;
+        if (WAYS == 1) {
+            if (ta < p.T)
+                load_cols<F32>(p, ta, nc, y[0]);
+            if (tb < p.T)
+                load_cols<F32>(p, tb, nc, y[1]);
+        }
+        if (way == 0) {
+            // tokens without an adapter
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (none >> (g + 8 * h) & 1) {
+                    if (WAYS > 1)
+                        load_cols<F32>(p, h ? tb : ta, nc, y[h]);
+                    store_cols<F32>(p, h ? tb : ta, nc, y[h]);
+                }
+            }
+        }
+        for (int ord = 0; firsts; ++ord, firsts &= firsts - 1) {
+            if (WAYS > 1 && ord % WAYS != way)
+                continue;
+            const int a = __shfl_sync(0xffffffffu, id, __ffs(firsts) - 1);
+            const unsigned rows = __ballot_sync(0xffffffffu, id == a);
+            const bool r0 = rows >> g & 1, r1 = rows >> (g + 8) & 1;
+            if (WAYS > 1) {
+                if (r0)
+                    load_cols<F32>(p, ta, nc, y[0]);
+                if (r1)
+                    load_cols<F32>(p, tb, nc, y[1]);
+            }
+            float acc[4][4] = {};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const int k = 16 * kb + 4 * c;                // this lane's four ranks
+                if (16 * kb >= p.r)
+                    break;
+                float4 ua = {}, ub = {};
+                uint2 b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // column g of tile i: 8 (g / 2) + 2 i + g % 2
+                    const int64_t n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
+                    b[i] = make_uint2(0, 0);
+                    if (k < p.r && n < p.N)
+                        b[i] = __ldg(reinterpret_cast<const uint2 *>(p.up + (int64_t(a) * p.N + n) * p.r + k));
+                }
+                if (k < p.r) {
+                    for (int z = 0; z < p.splits; ++z) {
+                        const float *u = p.u + int64_t(z) * p.T * p.r + k;
+                        if (r0) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(u + ta * p.r));
+                            ua = make_float4(ua.x + v.x, ua.y + v.y, ua.z + v.z, ua.w + v.w);
+                        }
+                        if (r1) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(u + tb * p.r));
+                            ub = make_float4(ub.x + v.x, ub.y + v.y, ub.z + v.z, ub.w + v.w);
+                        }
+                    }
+                }
+                constexpr int kTerms = F32 ? 3 : 2;
+                uint32_t w0[kTerms], w1[kTerms], w2[kTerms], w3[kTerms];
+                split_bf16(ua.x, ua.y, w0);
+                split_bf16(ub.x, ub.y, w1);
+                split_bf16(ua.z, ua.w, w2);
+                split_bf16(ub.z, ub.w, w3);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int s = kTerms - 1; s >= 0; --s)
+                        mma_bf16(acc[i], w0[s], w1[s], w2[s], w3[s], b[i].x, b[i].y);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h ? r1 : r0) {
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[2 * i] = y[h][2 * i] + acc[i][2 * h];
+                        f[2 * i + 1] = y[h][2 * i + 1] + acc[i][2 * h + 1];
+                    }
+                    store_cols<F32>(p, h ? tb : ta, nc, f);
+                }
+            }
+        }
+    }
+}
+
+// K splits of the first launch: enough CTAs for the GPU while each warp still
+// has a 32-k group (K >= 64; T is all the workspace's size may depend on, so
+// the splits go by the tokens and the launch takes no more than K allows).
+int max_splits(int64_t T, int sms)
+{
+    const int64_t tiles = (T + kTile - 1) / kTile;
+    return int(std::clamp<int64_t>(2 * sms / tiles, 1, 32));
+}
+
+cudaError_t launch(void (*kernel)(AdapterParams), dim3 grid, int threads, bool pdl, cudaStream_t s,
+                   const AdapterParams &p)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool F32, int WAYS>
+auto up_kernel(int r) -> void (*)(AdapterParams)
+{
+    return r <= 16   ? adapter_up_kernel<1, F32, WAYS>
+           : r <= 32 ? adapter_up_kernel<2, F32, WAYS>
+           : r <= 64 ? adapter_up_kernel<4, F32, WAYS>
+                     : adapter_up_kernel<8, F32, WAYS>;
 }
 
 }  // namespace
 
-size_t adapter_workspace_bytes(int64_t T, int r) { return size_t(T) * size_t(r) * sizeof(float); }
+size_t adapter_workspace_bytes(int64_t T, int r)
+{
+    const DeviceInfo *di = device_info();
+    return di ? size_t(max_splits(T, di->sm_count)) * size_t(T) * size_t(r) * sizeof(float) : 0;
+}
 
 int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
 {
     const DeviceInfo *di = device_info();
     if (!di)
         return BL_ERR_CUDA;
-    float *u = static_cast<float *>(a.ws);
-    const int64_t blocks = (a.T * a.r + 3) / 4;
-    if (blocks > 0x7fffffff)
-        return BL_ERR_SHAPE;
-    adapter_down_kernel<<<unsigned(blocks), 128, 0, s>>>(a, u, di->status);
-    int st = launch_status();
+    const int64_t tiles = (a.T + kTile - 1) / kTile;
+    const int esz = a.yt == BL_BF16 ? 2 : 4;
+    auto vec = [&](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * esz % 16 == 0; };
+    AdapterParams p{};
+    p.y = a.y;
+    p.ldy = a.ldy;
+    p.x = static_cast<const __nv_bfloat16 *>(a.x);
+    p.ldx = a.ldx;
+    p.T = a.T;
+    p.N = a.N;
+    p.K = a.K;
+    p.down = static_cast<const __nv_bfloat16 *>(a.down);
+    p.up = static_cast<const __nv_bfloat16 *>(a.up);
+    p.n = a.n;
+    p.r = a.r;
+    p.index = a.index;
+    p.scale = a.scale;
+    p.out = a.out;
+    p.ldo = a.ldo;
+    p.u = static_cast<float *>(a.ws);
+    p.splits = int(std::clamp<int64_t>(a.K / 32 / kDownWarps, 1, max_splits(a.T, di->sm_count)));
+    p.vec = vec(a.y, a.ldy) && vec(a.out, a.ldo);
+    p.status = di->status;
+    // a tile's adapters go to CTAs of their own while tiles alone do not fill the GPU
+    p.down_ways = int(std::clamp<int64_t>(di->sm_count / tiles, 1, std::min<int64_t>({kTile, a.n, a.T})));
+    auto down = a.r <= 8    ? adapter_down_kernel<1>
+                : a.r <= 16 ? adapter_down_kernel<2>
+                : a.r <= 32 ? adapter_down_kernel<4>
+                : a.r <= 64 ? adapter_down_kernel<8>
+                            : adapter_down_kernel<16>;
+    const dim3 dgrid(unsigned(tiles), unsigned(p.down_ways), unsigned(p.splits));
+    int st = cuda_status(launch(down, dgrid, kDownWarps * 32, a.flags & BL_FLAG_PDL, s, p));
     if (st)
         return st;
-    const dim3 grid(unsigned((a.N + 127) / 128), unsigned(a.T < 4096 ? a.T : 4096));
-    adapter_up_kernel<<<grid, 128, 0, s>>>(a, u);
-    return launch_status();
+    // few tokens: a CTA per 32 columns and 16 tokens, its warps share the adapters
+    const bool few = tiles * ((a.N + 8 * kUpCols - 1) / (8 * kUpCols)) < 2 * di->sm_count;
+    const int cols = few ? kUpCols : kUpWarps * kUpCols, tokens = few ? kTile : kUpTokens;
+    const int64_t gx = (a.N + cols - 1) / cols, gy = (a.T + tokens - 1) / tokens;
+    auto up = a.yt == BL_F32 ? (few ? up_kernel<true, 8>(a.r) : up_kernel<true, 1>(a.r))
+                             : (few ? up_kernel<false, 8>(a.r) : up_kernel<false, 1>(a.r));
+    return cuda_status(launch(up, dim3(unsigned(gx), unsigned(std::min<int64_t>(gy, 65535))), kUpWarps * 32, true, s, p));
 }
 
 }  // namespace bl

@@ -148,13 +148,15 @@ def test_rope_argument_errors_before_any_cuda_call(bl):
     def call(q=None, k=None, v=None, xt=1, H=2, Hkv=2, D=128, pos=A, tab=A, rows=64, qg=None, kg=None, gt=0, eps=1e-5,
              slots=None, qo=None, ko=None, vo=None, flags=0):
         d = _h(bl)
-        return L.bitlinear_qk_norm_rope(q or d, k or d, v or d, xt, H, Hkv, D, pos, tab, rows, qg, kg, gt, eps, slots,
-                                        qo or d, ko or d, vo or d, flags, None)
+        p = [ctypes.byref(h or d) for h in (q, k, v, qo, ko, vo)]
+        return L.bitlinear_qk_norm_rope(*p[:3], xt, H, Hkv, D, pos, tab, rows, qg, kg, gt, eps, slots, *p[3:], flags,
+                                        None)
 
     assert call(pos=None) == bl.BL_ERR_NULL
     assert call(v=_h(bl, data=0)) == bl.BL_ERR_NULL                # values without v, with v_out
-    assert L.bitlinear_qk_norm_rope(None, _h(bl), None, 1, 2, 2, 128, A, A, 64, None, None, 0, 1e-5, None, _h(bl),
-                                    _h(bl), None, 0, None) == bl.BL_ERR_NULL
+    d = ctypes.byref(_h(bl))
+    assert L.bitlinear_qk_norm_rope(None, d, None, 1, 2, 2, 128, A, A, 64, None, None, 0, 1e-5, None, d, d, None, 0,
+                                    None) == bl.BL_ERR_NULL
     assert call(xt=5) == bl.BL_ERR_DTYPE
     assert call(qg=A, gt=7) == bl.BL_ERR_DTYPE
     for kw in (dict(D=64), dict(H=0), dict(rows=0), dict(flags=2), dict(flags=64), dict(qg=A, eps=-1.0),
@@ -173,8 +175,8 @@ def test_attention_argument_errors_before_any_cuda_call(bl):
 
     def call(q=None, k=None, v=None, cu=A, batch=2, H=2, Hkv=2, D=128, scale=0.1, out=None, ws=A, n=1 << 40, flags=0):
         d = _h(bl)
-        return L.bitlinear_attention_prefill(q or d, k or d, v or d, cu, A, batch, H, Hkv, D, scale, out or d, ws, n,
-                                             flags, None)
+        p = [ctypes.byref(h or d) for h in (q, k, v, out)]
+        return L.bitlinear_attention_prefill(*p[:3], cu, A, batch, H, Hkv, D, scale, p[3], ws, n, flags, None)
 
     assert call(cu=None) == bl.BL_ERR_NULL
     assert call(out=_h(bl, data=0)) == bl.BL_ERR_NULL
