@@ -33,7 +33,6 @@ namespace {
 constexpr int kTile = 16;                 // tokens per tile (MMA M)
 constexpr int kDownWarps = 8, kUpWarps = 8;
 constexpr int kUpCols = 32;               // output columns per warp
-constexpr int kUpTokens = 64;             // tokens per CTA of the second launch (many tokens)
 
 struct AdapterParams {
     const void *y;
@@ -60,6 +59,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // The adapter of token t0 + lane (lanes 0 .. 15), -1: none; an id that does
@@ -172,25 +177,55 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
     }
 }
 
-// Eight consecutive columns n .. n + 7 of row t.
+// Eight consecutive columns n .. n + 7 of row t of y, as loaded: 16-byte
+// vectors, or one element after the other where rows are not aligned or end.
 template <bool F32>
-__device__ __forceinline__ void load_cols(const AdapterParams &p, int64_t t, int64_t n, float (&f)[8])
-{
-    const int64_t at = t * p.ldy + n;
-    if (p.vec && n + 8 <= p.N) {
-        load8<F32 ? BL_F32 : BL_BF16, true>(p.y, at, f);
-        return;
-    }
+struct Cols {
+    uint4 v[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const AdapterParams &p, int64_t t, int64_t n)
+    {
+        const int64_t at = t * p.ldy + n;
+        if (p.vec && n + 8 <= p.N) {
+            const char *src = static_cast<const char *>(p.y) + at * (F32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (n + i >= p.N)
-            f[i] = 0.0f;
-        else if (F32)
-            f[i] = __uint_as_float(ld_dep_u32(static_cast<const float *>(p.y) + at + i));
-        else
-            f[i] = __uint_as_float(ld_dep_u16(static_cast<const __nv_bfloat16 *>(p.y) + at + i) << 16);
+            for (int i = 0; i < (F32 ? 2 : 1); ++i)
+                v[i] = ld_dep_v4(src + 16 * i);
+            return;
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = 0;
+            if (n + i < p.N)
+                w[i] = F32 ? ld_dep_u32(static_cast<const float *>(p.y) + at + i)
+                           : ld_dep_u16(static_cast<const __nv_bfloat16 *>(p.y) + at + i);
+        }
+        if constexpr (F32) {
+            v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+            v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        }
     }
-}
+    __device__ __forceinline__ void floats(float (&f)[8]) const
+    {
+        const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        if constexpr (F32) {
+            const uint32_t z[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i] = __uint_as_float(w[i]);
+                f[4 + i] = __uint_as_float(z[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
 
 template <bool F32>
 __device__ __forceinline__ void store_cols(const AdapterParams &p, int64_t t, int64_t n, const float (&f)[8])
@@ -204,10 +239,8 @@ __device__ __forceinline__ void store_cols(const AdapterParams &p, int64_t t, in
         } else {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t *>(&b);
-            }
+            for (int i = 0; i < 4; ++i)
+                w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
             *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         return;
@@ -216,12 +249,6 @@ __device__ __forceinline__ void store_cols(const AdapterParams &p, int64_t t, in
     for (int i = 0; i < 8; ++i)
         if (n + i < p.N)
             store_y(p.out, F32 ? BL_F32 : BL_BF16, at + i, f[i]);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // The values (a, b) as sums of TERMS bf16 values, largest first.
@@ -236,114 +263,127 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[TERMS
     }
 }
 
-// out = y + up u.  A warp has 32 columns; WAYS = 1: the warps of a CTA lie side
-// by side and walk its 64 tokens; WAYS = 8: they share the columns and the 16
-// tokens' adapters.
+// out = y + up u for one run of TILES tiles and the columns of a CTA.  A warp
+// has 32 columns; WAYS = 1: the warps of a CTA lie side by side and take the
+// tiles one after the other, every tile's y in flight from the start;
+// WAYS = 8: they share 32 columns and the adapters of one tile.  The tiles' u
+// come to shared memory first, the K splits' parts added in order.
 template <int KB, bool F32, int WAYS>
-__global__ void __launch_bounds__(kUpWarps * 32, KB <= 2 ? 3 : 2) adapter_up_kernel(const AdapterParams p)
+__global__ void __launch_bounds__(kUpWarps * 32) adapter_up_kernel(const AdapterParams p)
 {
+    constexpr int kTiles = WAYS == 1 ? (F32 ? 2 : 4) : 1;
+    constexpr int kPitch = 16 * KB + 4;
+    __shared__ float u_s[kTiles * kTile][kPitch];
+    __shared__ int id_s[kTiles * kTile];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int way = WAYS == 1 ? 0 : warp;
     const int64_t n0 = (int64_t(blockIdx.x) * (kUpWarps / WAYS) + (WAYS == 1 ? warp : 0)) * kUpCols;
-    if (n0 >= p.N)
-        return;
     const int64_t nc = n0 + 8 * c;                            // this lane's output columns
-    constexpr int kTokens = WAYS == 1 ? kUpTokens : kTile;
-    const int64_t tiles = (p.T + kTile - 1) / kTile;
-    // this CTA's tiles: runs of kTokens / kTile, gridDim.y runs apart
-    for (int64_t i = 0;; ++i) {
-        const int64_t tile = (int64_t(blockIdx.y) + i / (kTokens / kTile) * gridDim.y) * (kTokens / kTile) +
-                             i % (kTokens / kTile);
-        if (tile >= tiles)
-            break;
-        const int64_t t0 = tile * kTile;
-        const int id = tile_id(p, t0, lane, false);
-        unsigned firsts = first_of(id, lane);
-        const unsigned none = __ballot_sync(0xffffffffu, lane < kTile && t0 + lane < p.T && id < 0);
-        float y[2][8];
-        const int64_t ta = t0 + g, tb = ta + 8;
-        if (WAYS == 1) {
-            if (ta < p.T)
-                load_cols<F32>(p, ta, nc, y[0]);
-            if (tb < p.T)
-                load_cols<F32>(p, tb, nc, y[1]);
+    const bool cols = n0 < p.N;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t run = blockIdx.y; run * kTiles * kTile < p.T; run += gridDim.y) {
+        const int64_t t0 = run * kTiles * kTile;
+        const int tokens = int(min(int64_t(kTiles * kTile), p.T - t0));
+        Cols<F32> y[kTiles][2];
+        if (cols) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (16 * i + 8 * h + g < tokens)
+                        y[i][h].load(p, t0 + 16 * i + 8 * h + g, nc);
         }
-        if (way == 0) {
-            // tokens without an adapter
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (none >> (g + 8 * h) & 1) {
-                    if (WAYS > 1)
-                        load_cols<F32>(p, h ? tb : ta, nc, y[h]);
-                    store_cols<F32>(p, h ? tb : ta, nc, y[h]);
-                }
-            }
+        __syncthreads();                                      // the last run's u has been used
+        if (threadIdx.x < kTiles * kTile) {
+            int id = threadIdx.x < tokens ? int(ld_dep_u32(p.index + t0 + threadIdx.x)) : -1;
+            id_s[threadIdx.x] = id < 0 || id >= p.n ? -1 : id;     // reported by the first launch
         }
-        for (int ord = 0; firsts; ++ord, firsts &= firsts - 1) {
-            if (WAYS > 1 && ord % WAYS != way)
-                continue;
-            const int a = __shfl_sync(0xffffffffu, id, __ffs(firsts) - 1);
-            const unsigned rows = __ballot_sync(0xffffffffu, id == a);
-            const bool r0 = rows >> g & 1, r1 = rows >> (g + 8) & 1;
-            if (WAYS > 1) {
-                if (r0)
-                    load_cols<F32>(p, ta, nc, y[0]);
-                if (r1)
-                    load_cols<F32>(p, tb, nc, y[1]);
+        for (int e = threadIdx.x; e < tokens * (p.r / 4); e += kUpWarps * 32) {
+            const int row = e / (p.r / 4), k = 4 * (e - row * (p.r / 4));
+            float4 s = {};
+            const float *u = p.u + (t0 + row) * p.r + k;
+#pragma unroll 8
+            for (int z = 0; z < p.splits; ++z) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(u + int64_t(z) * p.T * p.r));
+                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
             }
-            float acc[4][4] = {};
+            *reinterpret_cast<float4 *>(&u_s[row][k]) = s;
+        }
+        __syncthreads();
+        if (!cols)
+            continue;
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                const int k = 16 * kb + 4 * c;                // this lane's four ranks
-                if (16 * kb >= p.r)
-                    break;
-                float4 ua = {}, ub = {};
-                uint2 b[4];
+        for (int i = 0; i < kTiles; ++i) {
+            if (16 * i >= tokens)
+                break;
+            const int id = lane < kTile ? id_s[16 * i + lane] : -1;
+            unsigned firsts = first_of(id, lane);
+            const unsigned none = __ballot_sync(0xffffffffu, lane < tokens - 16 * i && lane < kTile && id < 0);
+            const int64_t ta = t0 + 16 * i + g, tb = ta + 8;
+            if (way == 0) {                                   // tokens without an adapter
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // column g of tile i: 8 (g / 2) + 2 i + g % 2
-                    const int64_t n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
-                    b[i] = make_uint2(0, 0);
-                    if (k < p.r && n < p.N)
-                        b[i] = __ldg(reinterpret_cast<const uint2 *>(p.up + (int64_t(a) * p.N + n) * p.r + k));
-                }
-                if (k < p.r) {
-                    for (int z = 0; z < p.splits; ++z) {
-                        const float *u = p.u + int64_t(z) * p.T * p.r + k;
-                        if (r0) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(u + ta * p.r));
-                            ua = make_float4(ua.x + v.x, ua.y + v.y, ua.z + v.z, ua.w + v.w);
-                        }
-                        if (r1) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(u + tb * p.r));
-                            ub = make_float4(ub.x + v.x, ub.y + v.y, ub.z + v.z, ub.w + v.w);
-                        }
+                for (int h = 0; h < 2; ++h) {
+                    if (none >> (g + 8 * h) & 1) {
+                        float f[8];
+                        y[i][h].floats(f);
+                        store_cols<F32>(p, h ? tb : ta, nc, f);
                     }
                 }
-                constexpr int kTerms = F32 ? 3 : 2;
-                uint32_t w0[kTerms], w1[kTerms], w2[kTerms], w3[kTerms];
-                split_bf16(ua.x, ua.y, w0);
-                split_bf16(ub.x, ub.y, w1);
-                split_bf16(ua.z, ua.w, w2);
-                split_bf16(ub.z, ub.w, w3);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int s = kTerms - 1; s >= 0; --s)
-                        mma_bf16(acc[i], w0[s], w1[s], w2[s], w3[s], b[i].x, b[i].y);
             }
+            for (int ord = 0; firsts; ++ord, firsts &= firsts - 1) {
+                if (WAYS > 1 && ord % WAYS != way)
+                    continue;
+                const int a = __shfl_sync(0xffffffffu, id, __ffs(firsts) - 1);
+                const unsigned rows = __ballot_sync(0xffffffffu, id == a);
+                const bool r0 = rows >> g & 1, r1 = rows >> (g + 8) & 1;
+                float acc[4][4] = {};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h ? r1 : r0) {
-                    float f[8];
+                for (int kb = 0; kb < KB; ++kb) {
+                    const int k = 16 * kb + 4 * c;            // this lane's four ranks
+                    if (16 * kb >= p.r)
+                        break;
+                    uint2 b[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f[2 * i] = y[h][2 * i] + acc[i][2 * h];
-                        f[2 * i + 1] = y[h][2 * i + 1] + acc[i][2 * h + 1];
+                    for (int x = 0; x < 4; ++x) {
+                        // column g of tile x: 8 (g / 2) + 2 x + g % 2
+                        const int64_t n = n0 + 8 * (g >> 1) + 2 * x + (g & 1);
+                        b[x] = make_uint2(0, 0);
+                        if (k < p.r && n < p.N)
+                            b[x] = __ldg(reinterpret_cast<const uint2 *>(p.up + (int64_t(a) * p.N + n) * p.r + k));
                     }
-                    store_cols<F32>(p, h ? tb : ta, nc, f);
+                    // rows of other adapters are dropped below; ranks behind r are zero
+                    float4 ua = {}, ub = {};
+                    if (k < p.r) {
+                        if (r0)
+                            ua = *reinterpret_cast<const float4 *>(&u_s[16 * i + g][k]);
+                        if (r1)
+                            ub = *reinterpret_cast<const float4 *>(&u_s[16 * i + g + 8][k]);
+                    }
+                    constexpr int kTerms = F32 ? 3 : 2;
+                    uint32_t w0[kTerms], w1[kTerms], w2[kTerms], w3[kTerms];
+                    split_bf16(ua.x, ua.y, w0);
+                    split_bf16(ub.x, ub.y, w1);
+                    split_bf16(ua.z, ua.w, w2);
+                    split_bf16(ub.z, ub.w, w3);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int s = kTerms - 1; s >= 0; --s)
+                            mma_bf16(acc[x], w0[s], w1[s], w2[s], w3[s], b[x].x, b[x].y);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h ? r1 : r0) {
+                        float f[8];
+                        y[i][h].floats(f);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            f[2 * x] += acc[x][2 * h];
+                            f[2 * x + 1] += acc[x][2 * h + 1];
+                        }
+                        store_cols<F32>(p, h ? tb : ta, nc, f);
+                    }
                 }
             }
         }
@@ -432,7 +472,7 @@ int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
         return st;
     // few tokens: a CTA per 32 columns and 16 tokens, its warps share the adapters
     const bool few = tiles * ((a.N + 8 * kUpCols - 1) / (8 * kUpCols)) < 2 * di->sm_count;
-    const int cols = few ? kUpCols : kUpWarps * kUpCols, tokens = few ? kTile : kUpTokens;
+    const int cols = few ? kUpCols : kUpWarps * kUpCols, tokens = kTile * (few ? 1 : a.yt == BL_F32 ? 2 : 4);
     const int64_t gx = (a.N + cols - 1) / cols, gy = (a.T + tokens - 1) / tokens;
     auto up = a.yt == BL_F32 ? (few ? up_kernel<true, 8>(a.r) : up_kernel<true, 1>(a.r))
                              : (few ? up_kernel<false, 8>(a.r) : up_kernel<false, 1>(a.r));

@@ -66,7 +66,7 @@ constexpr uint32_t kTile = 2 * kBox;      // 128 x 128 bf16
 constexpr int kItems = 4;                 // work list ring
 constexpr float kRescale = 8.0f;          // log2 of the growth of a row's weights before O is rescaled
 // Registers: 168 a thread at launch; a softmax thread holds its row of S.
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 
 // Instruction descriptors: D fp32, A and B bf16, M = N = 128; B is K-major for
@@ -92,7 +92,7 @@ struct Item {
 };
 
 // What the joining kernel needs about the tile whose first part a CTA holds.
-struct JoinHeader {
+struct alignas(16) JoinHeader {
     int valid;
     int kvh, q_row, toks;
     int last;               // CTA of the last part
@@ -413,6 +413,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             int it = 0, loads = 0;       // pieces listed, blocks loaded
             int q_loads = 0;
             bool ok = true;
+            auto load_q = [&](const Item &item) {
+                if (!BL_WAIT(sm.q_empty, (uint32_t(q_loads) & 1u) ^ 1u))
+                    return false;
+                ++q_loads;
+                const int qt = PAIR && item.toks > p.TM ? 2 : 1;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&sm.q_full);
+                    mbar_arrive_tx(bar, uint32_t(qt * p.TM * p.G) * 256u);
+                    for (int s = 0; s < qt; ++s) {
+                        const uint32_t dst = smem_u32(sm.q[s]);
+                        tma_load_3d(dst, &qmap, bar, 0, item.kvh * p.G, item.q_row + s * p.TM);
+                        tma_load_3d(dst + kBox, &qmap, bar, 64, item.kvh * p.G, item.q_row + s * p.TM);
+                    }
+                }
+                __syncwarp();
+                return true;
+            };
             for (; ok; ++it) {
                 const int islot = it % kItems;
                 if (!BL_WAIT(sm.item_empty[islot], (uint32_t(it / kItems) & 1u) ^ 1u))
@@ -473,24 +490,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     break;
                 if (item.n == 0)
                     continue;
-                // queries (once every score product of the previous piece is complete)
-                if (!BL_WAIT(sm.q_empty, (uint32_t(q_loads) & 1u) ^ 1u))
-                    break;
-                ++q_loads;
-                const int qt = PAIR && item.toks > p.TM ? 2 : 1;
-                if (lane == 0) {
-                    const uint32_t bar = smem_u32(&sm.q_full);
-                    mbar_arrive_tx(bar, uint32_t(qt * p.TM * p.G) * 256u);
-                    for (int s = 0; s < qt; ++s) {
-                        const uint32_t dst = smem_u32(sm.q[s]);
-                        tma_load_3d(dst, &qmap, bar, 0, item.kvh * p.G, item.q_row + s * p.TM);
-                        tma_load_3d(dst + kBox, &qmap, bar, 64, item.kvh * p.G, item.q_row + s * p.TM);
-                    }
-                }
-                __syncwarp();
-                // blocks in the order in which the products take them
+                // The piece's blocks in the order in which the products take
+                // them.  The first ones are asked for before the queries, whose
+                // place is free only when every score product of the previous
+                // piece is complete: their stages come free without these
+                // queries, so the ring never waits for itself.
                 const int n = item.n, masked = max(0, min(item.nk, item.lim0)) / kKeys - item.j0;
-                for (int x = 0; x < 2 * n; ++x, ++loads) {
+                const int early = min(2 * n, kStages - 2);
+                for (int x = 0; x < 2 * n && ok; ++x, ++loads) {
+                    if (x == early)
+                        ok = load_q(item);
                     bool is_v;
                     int i;
                     if (PAIR) {
@@ -506,10 +515,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         i = y > 2 * (n - 2) ? y - max(0, n - 2) : is_v ? y / 2 : y / 2 + 2;
                     }
                     const int st = loads % kStages;
-                    if (!BL_WAIT(sm.kv_empty[st], (uint32_t(loads / kStages) & 1u) ^ 1u)) {
-                        ok = false;
+                    ok = ok && BL_WAIT(sm.kv_empty[st], (uint32_t(loads / kStages) & 1u) ^ 1u);
+                    if (!ok)
                         break;
-                    }
                     if (lane == 0) {
                         const uint32_t bar = smem_u32(&sm.kv_full[st]), dst = smem_u32(sm.kv[st]);
                         const CUtensorMap *map = is_v ? &vmap : &kmap;
@@ -522,6 +530,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     }
                     __syncwarp();
                 }
+                if (ok && early == 2 * n)
+                    ok = load_q(item);
             }
             // copies in flight have landed before the CTA exits (at once
             // unless another role gave up before it took them)
@@ -939,87 +949,100 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 // ---------------------------------------------------------------- joining the parts of cut tiles
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinSplit = 4;        // CTAs per cut tile
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinSplit = 16;       // CTAs per cut tile
+constexpr int kJoinFew = 8;          // up to so many parts, a warp has a row to itself
+constexpr int kJoinLanes = 8;        // parts per lane: grids of up to 256 CTAs
 
-// CTA (c, y) takes every kJoinSplit-th row of the tile whose first part CTA c
-// of the main kernel holds.  `span` warps share a row's parts (as many as
-// there are parts, up to all of them), each adding its own in order, then the
-// warps' sums are added in order.
+// CTA (c, y) takes every kJoinSplit-th row, or group of rows, of the tile
+// whose first part CTA c of the main kernel holds.  All of a row's (m, l) come
+// with one load per lane, then its O's with independent loads: few parts
+// (prompts), a warp per row; many (a long cache cut over the GPU), the CTA's
+// warps share a row's parts and add their sums in order.
 template <bool PAIR>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const PrefillParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int kWarps = kJoinThreads / 32;
-    __shared__ float4 acc_s[kWarps][32];
-    __shared__ float l_s[kWarps], m_s[kWarps];
+    __shared__ float4 acc_s[kJoinWarps][32];
+    __shared__ float fac_s[32 * kJoinLanes];
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (!ld_dep_u32(&p.hdr[c].valid))
+    const uint4 h0 = ld_dep_v4(&p.hdr[c]), h1 = ld_dep_v4(&p.hdr[c].last);
+    if (!h0.x)
         return;
-    const JoinHeader h{1, int(ld_dep_u32(&p.hdr[c].kvh)), int(ld_dep_u32(&p.hdr[c].q_row)),
-                       int(ld_dep_u32(&p.hdr[c].toks)), int(ld_dep_u32(&p.hdr[c].last)), {}};
-    const int parts = h.last - c + 1;
-    int span = 1;
-    while (span < parts && span < kWarps)
-        span *= 2;
+    const int kvh = int(h0.y), q_row = int(h0.z), toks = int(h0.w), parts = int(h1.x) - c + 1;
     constexpr int64_t kSlotRows = PAIR ? 2 * kRows : kRows;
-    const int rows = h.toks * p.G, team = warp / span, in = warp % span;
-    auto slot_of = [&](int i) { return int64_t(i ? 2 * (c + i) : 2 * c + 1); };
-    for (int base = blockIdx.y * (kWarps / span); base < rows; base += kJoinSplit * (kWarps / span)) {
-        const int row = base + team;                        // token * G + head of the group
-        const bool here = row < rows;
-        const int tok = row / p.G, g = row - tok * p.G;
+    const int rows = toks * p.G;
+    const bool few = parts <= kJoinFew;
+    const int step = few ? kJoinSplit * kJoinWarps : kJoinSplit;
+    for (int row = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; row < rows; row += step) {
+        const int tok = row / p.G, g = row - tok * p.G;     // token of the tile, head of the group
         const int tile = PAIR ? tok / p.TM : 0;             // stream
         const int64_t at = tile * kRows + (tok - tile * p.TM) * p.G + g;
-        float m = -INFINITY, l = 0.0f;
+        // part i: the first is the slot of a tile's beginning, the others of a continuation
+        auto part_row = [&](int i) { return int64_t(i ? 2 * (c + i) : 2 * c + 1) * kSlotRows + at; };
+        float m = -INFINITY, pm[kJoinLanes], pl[kJoinLanes];
+#pragma unroll
+        for (int x = 0; x < kJoinLanes; ++x) {
+            const int i = 32 * x + lane;
+            const float2 ml = i < parts ? __ldcg(&p.part_ml[part_row(i)]) : make_float2(-INFINITY, 0.0f);
+            pm[x] = ml.x;
+            pl[x] = ml.y;
+            m = fmaxf(m, ml.x);
+        }
+        m = warp_max(m);
+        float l = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kJoinLanes; ++x) {
+            // the part's factor; a part without a visible key has none (its O is not written).
+            // NaN scores leave m at -inf and l NaN: the factor is NaN then
+            const float f = pl[x] == 0.0f ? 0.0f : exp2f((pm[x] - m) * p.c);
+            l = fmaf(pl[x], f, l);
+            pm[x] = f;
+        }
+        l = warp_sum(l);
         float4 acc = {};
-        if (here) {
-            for (int i = in; i < parts; i += span)
-                m = fmaxf(m, __ldcg(&p.part_ml[slot_of(i) * kSlotRows + at]).x);
+        auto add = [&](int i, float f) {
+            if (f == 0.0f)
+                return;
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + part_row(i) * kHD) + lane);
+            acc.x = fmaf(o.x, f, acc.x);
+            acc.y = fmaf(o.y, f, acc.y);
+            acc.z = fmaf(o.z, f, acc.z);
+            acc.w = fmaf(o.w, f, acc.w);
+        };
+        if (few) {
+#pragma unroll
+            for (int i = 0; i < kJoinFew; ++i)
+                if (i < parts)
+                    add(i, __shfl_sync(0xffffffffu, pm[0], i));
+        } else {
+            if (warp == 0) {
+#pragma unroll
+                for (int x = 0; x < kJoinLanes; ++x)
+                    fac_s[32 * x + lane] = pm[x];
+            }
+            __syncthreads();
 #pragma unroll 4
-            for (int i = in; i < parts; i += span) {
-                const int64_t pr = slot_of(i) * kSlotRows + at;
-                const float2 ml = __ldcg(&p.part_ml[pr]);
-                if (ml.x == -INFINITY && ml.y == 0.0f)
-                    continue;                               // no visible key in this part
-                const float f = exp2f((ml.x - m) * p.c);
-                const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * kHD) + lane);
-                l = fmaf(ml.y, f, l);
-                acc.x = fmaf(o.x, f, acc.x);
-                acc.y = fmaf(o.y, f, acc.y);
-                acc.z = fmaf(o.z, f, acc.z);
-                acc.w = fmaf(o.w, f, acc.w);
+            for (int i = warp; i < parts; i += kJoinWarps)
+                add(i, fac_s[i]);
+            acc_s[warp][lane] = acc;
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    const float4 o = acc_s[w][lane];
+                    acc = make_float4(acc.x + o.x, acc.y + o.y, acc.z + o.z, acc.w + o.w);
+                }
             }
+            __syncthreads();
+            if (warp)
+                continue;
         }
-        acc_s[warp][lane] = acc;
-        if (lane == 0) {
-            l_s[warp] = l;
-            m_s[warp] = m;
-        }
-        __syncthreads();
-        if (here && in == 0) {
-            for (int i = 1; i < span; ++i)
-                m = fmaxf(m, m_s[warp + i]);
-            l = 0.0f;
-            acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int i = 0; i < span; ++i) {
-                const float mi = m_s[warp + i];
-                const float f = mi == -INFINITY ? 0.0f : exp2f((mi - m) * p.c);
-                const float4 o = acc_s[warp + i][lane];
-                if (mi == -INFINITY && l_s[warp + i] == 0.0f)
-                    continue;
-                l = fmaf(l_s[warp + i], f, l);
-                acc.x = fmaf(o.x, f, acc.x);
-                acc.y = fmaf(o.y, f, acc.y);
-                acc.z = fmaf(o.z, f, acc.z);
-                acc.w = fmaf(o.w, f, acc.w);
-            }
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            __nv_bfloat16 *dst = p.out + int64_t(h.q_row + tok) * p.o_row + int64_t(h.kvh * p.G + g) * p.o_head;
-            *reinterpret_cast<uint2 *>(dst + 4 * lane) =
-                make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
-        }
-        __syncthreads();
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        __nv_bfloat16 *dst = p.out + int64_t(q_row + tok) * p.o_row + int64_t(kvh * p.G + g) * p.o_head;
+        *reinterpret_cast<uint2 *>(dst + 4 * lane) =
+            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
     }
 }
 
@@ -1055,6 +1078,8 @@ int make_map(CUtensorMap *map, const bitlinear_heads &h, int heads, uint32_t box
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? BL_OK : BL_ERR_CUDA;
 }
+
+int main_grid(const DeviceInfo *di) { return std::min(di->sm_count, 32 * kJoinLanes); }
 
 // Workspace: a join header per CTA, then the parts' m and l, then their O.
 struct WsLayout {
@@ -1104,7 +1129,7 @@ int launch_mode(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap 
 size_t attention_prefill_workspace_bytes(int, int)
 {
     const DeviceInfo *di = device_info();
-    return di ? ws_layout(di->sm_count).total : 0;
+    return di ? ws_layout(main_grid(di)).total : 0;
 }
 
 int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s)
@@ -1112,7 +1137,7 @@ int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s)
     const DeviceInfo *di = device_info();
     if (!di)
         return BL_ERR_CUDA;
-    const int grid = di->sm_count, G = a.H / a.Hkv;
+    const int grid = main_grid(di), G = a.H / a.Hkv;
     const WsLayout w = ws_layout(grid);
     auto *base = static_cast<unsigned char *>(a.ws);
     PrefillParams p{};

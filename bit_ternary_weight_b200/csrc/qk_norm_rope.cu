@@ -14,7 +14,11 @@
 // take a head, each with dimensions 8c .. 8c + 7 and 64 + 8c .. 64 + 8c + 7, so
 // that every load and store of bf16 is 16 bytes a lane and 128 contiguous
 // bytes a head, and both kinds of pairs ((2i, 2i + 1) and (i, i + 64)) are
-// inside one lane; the mean square is a sum over three shuffles.
+// inside one lane; the mean square is a sum over three shuffles.  A warp takes
+// four heads at a time of one token, whose angles stay in registers, and asks
+// for several steps' heads before it knows the token's position.
+#include <algorithm>
+
 #include "bl_common.cuh"
 
 namespace bl {
@@ -30,6 +34,7 @@ struct RopeParams {
     __nv_bfloat16 *qo, *ko, *vo;
     int64_t qo_row, qo_head, ko_row, ko_head, vo_row, vo_head;
     int T, H, Hkv, heads;          // heads: H + Hkv (+ Hkv with values)
+    int parts, steps;              // warps per token, steps of four heads each takes
     const int32_t *positions;
     const float2 *table;
     int64_t table_rows;
@@ -45,10 +50,41 @@ struct RopeParams {
 __device__ __forceinline__ void gain8(const void *g, int gt, int at, float f[8])
 {
     if (gt == BL_BF16)
-        load8<BL_BF16, true>(g, at, f);
+        load8<BL_BF16>(g, at, f);
     else
-        load8<BL_F32, true>(g, at, f);
+        load8<BL_F32>(g, at, f);
 }
+
+// Eight elements as loaded: one 16-byte vector of bf16, two of fp32.
+template <int XT>
+struct Raw8 {
+    uint4 v[XT == BL_BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *base, int64_t at)
+    {
+        if constexpr (XT == BL_BF16) {
+            v[0] = ld_dep_v4(static_cast<const __nv_bfloat16 *>(base) + at);
+        } else {
+            v[0] = ld_dep_v4(static_cast<const float *>(base) + at);
+            v[1] = ld_dep_v4(static_cast<const float *>(base) + at + 4);
+        }
+    }
+    __device__ __forceinline__ void floats(float f[8]) const
+    {
+        if constexpr (XT == BL_BF16) {
+            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+            const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] = __uint_as_float(w[i]);
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
@@ -72,78 +108,99 @@ __device__ __forceinline__ void rotate(float &a, float &b, float2 cs)
 template <int XT, bool HALVES>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams p)
 {
+    constexpr int kAhead = XT == BL_BF16 ? 4 : 2;        // steps whose heads are in flight
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t item = (int64_t(blockIdx.x) * kRopeThreads + threadIdx.x) / kHeadLanes;
-    const int c = threadIdx.x % kHeadLanes;
-    const int64_t t = item / p.heads;
-    const int h = int(item - t * p.heads);
+    const int64_t item = (int64_t(blockIdx.x) * kRopeThreads + threadIdx.x) / 32;
+    const int64_t t = item / p.parts;
     if (t >= p.T)
-        return;     // whole groups of eight lanes; the shuffles below name their group only
-    const unsigned group = 0xffu << (threadIdx.x & 24);
-    const bool is_q = h < p.H, is_k = !is_q && h < p.H + p.Hkv;
-    const int64_t pos = int32_t(ld_dep_u32(p.positions + t));
-    if (pos < 0 || pos >= p.table_rows) {
-        if (h == 0 && c == 0)
-            atomicExch(p.status, BL_ERR_SHAPE);
         return;
-    }
-    int64_t row = t;
-    if (!is_q && p.slots) {
-        row = int32_t(ld_dep_u32(p.slots + t));
-        if (row < 0)
+    const int lane = threadIdx.x & 31, c = lane % kHeadLanes;
+    const int first = int(item - t * p.parts) * p.steps * 4 + lane / kHeadLanes;     // this lane's first head
+    const int last = min(p.heads, (int(item - t * p.parts) + 1) * p.steps * 4);
+    Raw8<XT> lo[kAhead], hi[kAhead];
+    auto load = [&](int h, Raw8<XT> &a, Raw8<XT> &b) {
+        if (h >= last)
             return;
-        if (row >= p.out_rows) {
-            if (c == 0)
-                atomicExch(p.status, BL_ERR_SHAPE);
+        const void *src = h < p.H ? p.q : h < p.H + p.Hkv ? p.k : p.v;
+        const int64_t at = h < p.H            ? t * p.q_row + h * p.q_head
+                           : h < p.H + p.Hkv ? t * p.k_row + (h - p.H) * p.k_head
+                                              : t * p.v_row + (h - p.H - p.Hkv) * p.v_head;
+        a.load(src, at + 8 * c);
+        b.load(src, at + 64 + 8 * c);
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        load(first + 4 * u, lo[u], hi[u]);
+    const int64_t pos = int32_t(ld_dep_u32(p.positions + t));
+    int64_t row = p.slots ? int32_t(ld_dep_u32(p.slots + t)) : t;
+    const bool bad_pos = pos < 0 || pos >= p.table_rows, bad_row = p.slots && row >= p.out_rows;
+    if (bad_pos || bad_row) {
+        if (lane == 0)
+            atomicExch(p.status, BL_ERR_SHAPE);
+        if (bad_pos)
             return;
-        }
+        row = -1;
     }
-    const int hk = is_q ? h : is_k ? h - p.H : h - p.H - p.Hkv;
-    const void *src = is_q ? p.q : is_k ? p.k : p.v;
-    const int64_t at = is_q ? t * p.q_row + hk * p.q_head : is_k ? t * p.k_row + hk * p.k_head : t * p.v_row + hk * p.v_head;
-    __nv_bfloat16 *dst = is_q   ? p.qo + row * p.qo_row + hk * p.qo_head
-                         : is_k ? p.ko + row * p.ko_row + hk * p.ko_head
-                                : p.vo + row * p.vo_row + hk * p.vo_head;
-    float lo[8], hi[8];
-    load8<XT, true>(src, at + 8 * c, lo);
-    load8<XT, true>(src, at + 64 + 8 * c, hi);
-    if (is_q || is_k) {
-        const void *gain = is_q ? p.q_gain : p.k_gain;
-        if (gain) {
+    // (cos, sin) of this lane's pairs: 8c .. 8c + 7, or 4c .. 4c + 3 and 32 + 4c .. 32 + 4c + 3
+    const float2 *tab = p.table + pos * (kHD / 2);
+    float2 cs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        cs[i] = __ldg(tab + (HALVES ? 8 * c + i : i < 4 ? 4 * c + i : 32 + 4 * c + i - 4));
+    for (int h0 = first; h0 - lane / kHeadLanes < last; h0 += 4 * kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int h = h0 + 4 * u;
+            if (h - lane / kHeadLanes >= last)
+                break;
+            float a[8], b[8];
+            lo[u].floats(a);
+            hi[u].floats(b);
+            const bool is_q = h < p.H, is_k = !is_q && h < p.H + p.Hkv;
+            const void *gain = is_q ? p.q_gain : is_k ? p.k_gain : nullptr;
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                s = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], s));
+                s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
 #pragma unroll
             for (int o = kHeadLanes / 2; o > 0; o >>= 1)
-                s += __shfl_xor_sync(group, s, o);
-            const float r = __fdiv_rn(1.0f, __fsqrt_rn(s * (1.0f / kHD) + p.eps));
-            float g[8];
-            gain8(gain, p.gt, 8 * c, g);
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+            load(h + 4 * kAhead, lo[u], hi[u]);
+            if (h >= last || (!is_q && row < 0))
+                continue;
+            if (gain) {
+                const float r = __fdiv_rn(1.0f, __fsqrt_rn(s * (1.0f / kHD) + p.eps));
+                float g[8];
+                gain8(gain, p.gt, 8 * c, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                lo[i] = lo[i] * r * g[i];
-            gain8(gain, p.gt, 64 + 8 * c, g);
+                for (int i = 0; i < 8; ++i)
+                    a[i] = a[i] * r * g[i];
+                gain8(gain, p.gt, 64 + 8 * c, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                hi[i] = hi[i] * r * g[i];
-        }
-        const float2 *tab = p.table + pos * (kHD / 2);
-        if (HALVES) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                rotate(lo[i], hi[i], __ldcg(tab + 8 * c + i));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                rotate(lo[2 * i], lo[2 * i + 1], __ldcg(tab + 4 * c + i));
-                rotate(hi[2 * i], hi[2 * i + 1], __ldcg(tab + 32 + 4 * c + i));
+                for (int i = 0; i < 8; ++i)
+                    b[i] = b[i] * r * g[i];
             }
+            if (is_q || is_k) {
+                if (HALVES) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        rotate(a[i], b[i], cs[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        rotate(a[2 * i], a[2 * i + 1], cs[i]);
+                        rotate(b[2 * i], b[2 * i + 1], cs[4 + i]);
+                    }
+                }
+            }
+            __nv_bfloat16 *dst = is_q   ? p.qo + t * p.qo_row + h * p.qo_head
+                                 : is_k ? p.ko + row * p.ko_row + (h - p.H) * p.ko_head
+                                        : p.vo + row * p.vo_row + (h - p.H - p.Hkv) * p.vo_head;
+            *reinterpret_cast<uint4 *>(dst + 8 * c) = pack8(a);
+            *reinterpret_cast<uint4 *>(dst + 64 + 8 * c) = pack8(b);
         }
     }
-    *reinterpret_cast<uint4 *>(dst + 8 * c) = pack8(lo);
-    *reinterpret_cast<uint4 *>(dst + 64 + 8 * c) = pack8(hi);
 }
 
 }  // namespace
@@ -186,8 +243,13 @@ int launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t s)
     p.slots = a.slots;
     p.out_rows = a.k_out.rows;
     p.status = di->status;
-    const int64_t items = int64_t(p.T) * p.heads;
-    const int64_t blocks = (items * kHeadLanes + kRopeThreads - 1) / kRopeThreads;
+    // a token's heads go to one warp where the tokens fill the GPU (two
+    // CTAs' warps per SM and more), else to as many as there are steps
+    const int all = (p.heads + 3) / 4;
+    p.parts = int(std::clamp<int64_t>(int64_t(di->sm_count) * 16 / p.T, 1, all));
+    p.steps = (all + p.parts - 1) / p.parts;
+    p.parts = (all + p.steps - 1) / p.steps;
+    const int64_t blocks = (int64_t(p.T) * p.parts * 32 + kRopeThreads - 1) / kRopeThreads;
     if (blocks > 0x7fffffff)
         return BL_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
