@@ -64,6 +64,7 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10;
 constexpr uint32_t kBox = 128 * 128;      // 64 columns x 128 rows of bf16, one swizzle span wide
 constexpr uint32_t kTile = 2 * kBox;      // 128 x 128 bf16
 constexpr int kItems = 4;                 // work list ring
+constexpr int kTileExtra = 2;             // what a tile costs besides its key blocks, in key blocks
 constexpr float kRescale = 8.0f;          // log2 of the growth of a row's weights before O is rescaled
 // Registers: 168 a thread at launch; a softmax thread holds its row of S.
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
@@ -123,7 +124,8 @@ struct Smem {
     uint64_t v_fixed[kStages];
     uint64_t q_full, q_empty;
     uint64_t s_full[2];      // scores complete (and every earlier product)
-    uint64_t p_full[2];      // weights written over the scores
+    uint64_t p_half[2];      // weights of the first 64 keys written over the scores
+    uint64_t p_full[2];      // all of them
     uint64_t o_full[2];      // last product of the piece complete
     uint64_t ml_full;        // alt: stream 1's m and l are in ml
     uint64_t o1_read;        // alt: stream 1's O has been read
@@ -185,26 +187,21 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b)
         : "memory");
 }
 
-// Weights (tensor memory) times values: eight MMAs over the 128 keys, 16 keys
-// (two 8-row groups, 2048 bytes) each.
+// Weights (tensor memory) times values: four MMAs over 64 keys, 16 keys (two
+// 8-row groups, 2048 bytes) each.
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate)
 {
     asm volatile(
         "{\n\t.reg .pred e, p, t;\n\t.reg .b32 r;\n\t"
         "mov.u32 r, %%laneid;\n\t"
         "setp.eq.u32 e, r, 0;\n\t"
-        "setp.ne.b32 p, %18, 0;\n\t"
-        "setp.eq.b32 t, %18, %18;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %9, %17, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %10, %17, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %11, %17, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %12, %17, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %13, %17, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%6], %14, %17, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %15, %17, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%8], %16, %17, t;\n\t}" ::"r"(d),
-        "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "r"(a + 32), "r"(a + 40), "r"(a + 48), "r"(a + 56), "l"(b),
-        "l"(b + 128), "l"(b + 256), "l"(b + 384), "l"(b + 512), "l"(b + 640), "l"(b + 768), "l"(b + 896),
+        "setp.ne.b32 p, %10, 0;\n\t"
+        "setp.eq.b32 t, %10, %10;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b), "l"(b + 128), "l"(b + 256), "l"(b + 384),
         "r"(kIdescPV), "r"(accumulate)
         : "memory");
 }
@@ -221,6 +218,111 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Pairs of fp32 values in one register pair.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 2^x of two values, -inf < x <= 127, on the FMA pipe: x = n + f with n the
+// nearest integer (adding 1.5 * 2^23 leaves it in the low bits), 2^f by the
+// cubic whose relative error on [-1/2, 1/2] is least (7.5e-5 = 2^-13.7, found
+// by linear programming on that error; bf16 weights round at 2^-9), and n
+// added to the exponent.  Below 2^-126 the result is some value under 2^-125.
+__device__ __forceinline__ void exp2_fma(uint64_t x, float &lo, float &hi)
+{
+    const uint64_t big = pack_f32x2(12582912.0f, 12582912.0f), neg = pack_f32x2(-12582912.0f, -12582912.0f);
+    float a, b;
+    unpack_f32x2(x, a, b);
+    x = pack_f32x2(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+    const uint64_t n = add_f32x2(x, big);
+    const uint64_t f = fma_f32x2(add_f32x2(n, neg), pack_f32x2(-1.0f, -1.0f), x);
+    uint64_t p = fma_f32x2(f, pack_f32x2(0.0551716685295105f, 0.0551716685295105f),
+                           pack_f32x2(0.2426111251115799f, 0.2426111251115799f));
+    p = fma_f32x2(p, f, pack_f32x2(0.6932609677314758f, 0.6932609677314758f));
+    p = fma_f32x2(p, f, pack_f32x2(0.9999280571937561f, 0.9999280571937561f));
+    float pa, pb, na, nb;
+    unpack_f32x2(p, pa, pb);
+    unpack_f32x2(n, na, nb);
+    lo = __int_as_float(__float_as_int(pa) + (__float_as_int(na) << 23));
+    hi = __int_as_float(__float_as_int(pb) + (__float_as_int(nb) << 23));
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The weights of one row's scores, written over them as bf16: the first 64
+// keys' are handed on (`half`) while the others are computed.  Returns their
+// sum.  The exponentials are most of the work, and the unit that computes
+// them (4 a clock and quarter SM) would bind the kernel at the tensor cores'
+// own pace, so every kPoly-th pair goes to the FMA pipe instead; not in a
+// masked block, where a weight has to be zero exactly.
+constexpr int kPoly = 4;
+
+template <bool MASKED>
+__device__ __forceinline__ float row_weights(const uint32_t (&v)[128], float c, float mc, uint32_t s_tmem,
+                                             uint32_t half)
+{
+    const uint64_t c2 = pack_f32x2(c, c), m2 = pack_f32x2(-mc, -mc);
+    uint64_t sum[2] = {0, 0};       // two pairs of zeros
+    uint32_t w[2][32];
+    auto pair = [&](int x) {
+        const uint64_t t = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), c2, m2);
+        float a, b;
+        if (!MASKED && x % kPoly == kPoly - 1) {
+            exp2_fma(t, a, b);
+        } else {
+            unpack_f32x2(t, a, b);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+        }
+        sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(a, b));
+        w[x / 32][x % 32] = bf16x2(a, b);
+    };
+#pragma unroll
+    for (int x = 0; x < 32; ++x)
+        pair(x);
+    tmem_st32(s_tmem, w[0]);
+#pragma unroll
+    for (int x = 32; x < 40; ++x)
+        pair(x);
+    tmem_wait_st();
+    tmem_keep32(w[0]);
+    tc_fence_before();
+    mbar_arrive(half);
+#pragma unroll
+    for (int x = 40; x < 64; ++x)
+        pair(x);
+    tmem_st32_wait(s_tmem + 32, w[1]);
+    float s0, s1;
+    unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
+    return s0 + s1;
 }
 
 // ---------------------------------------------------------------- the work line
@@ -245,12 +347,22 @@ __device__ __forceinline__ int tile_blocks(int t0, int tt, int nq, int nk)
     return seen <= 0 ? 0 : int((seen + kKeys - 1) / kKeys);
 }
 
-// The same in units of the work line: a tile without keys still is one.
-__device__ __forceinline__ int64_t head_units(int tt, int nq, int nk)
+// Length of a tile on the work line: its blocks (one where there are none) and
+// `extra` for what a tile costs besides (queries, epilogue).
+__device__ __forceinline__ int tile_units(int blocks, int extra) { return max(1, blocks) + extra; }
+
+// The block at unit x of a tile.  With 1 + extra units to a CTA or more, no
+// CTA's share of a tile is without a block.
+__device__ __forceinline__ int unit_block(int64_t x, int blocks, int extra)
+{
+    return int(x * blocks / tile_units(blocks, extra));
+}
+
+__device__ __forceinline__ int64_t head_units(int tt, int nq, int nk, int extra)
 {
     int64_t u = 0;
     for (int64_t t0 = 0; t0 < nq; t0 += tt)
-        u += max(1, tile_blocks(int(t0), tt, nq, nk));
+        u += tile_units(tile_blocks(int(t0), tt, nq, nk), extra);
     return u;
 }
 
@@ -321,6 +433,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         mbar_init(smem_u32(&sm.q_empty), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sm.s_full[s]), 1);
+            mbar_init(smem_u32(&sm.p_half[s]), 128);
             mbar_init(smem_u32(&sm.p_full[s]), 128);
             mbar_init(smem_u32(&sm.o_full[s]), 1);
         }
@@ -354,18 +467,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         if (warp == kLoadWarp) {
             // ---------------------------------------- work list, TMA loads
             const int TT = PAIR ? 2 * p.TM : p.TM;        // tokens of a tile
-            int64_t W = 0;
+            int64_t W = 0, tiles = 0;
             bool bad = false;
             for (int b0 = 0; b0 < p.batch; b0 += 32) {
                 int q0, nq = 0, k0, nk = 0;
                 if (b0 + lane < p.batch) {
                     bad |= !sequence(p, b0 + lane, q0, nq, k0, nk);
-                    W += head_units(TT, nq, nk);
+                    W += head_units(TT, nq, nk, 0);
+                    tiles += (nq + TT - 1) / TT;
                 }
             }
             W = warp_sum64(W) * p.Hkv;
+            tiles = warp_sum64(tiles) * p.Hkv;
             if (bad && blockIdx.x == 0)
                 atomicExch(p.status, BL_ERR_SHAPE);
+            // short shares go by their blocks alone
+            const int extra = W >= 8 * int64_t(gridDim.x) ? kTileExtra : 0;
+            W += extra * tiles;
             const int64_t G = min(int64_t(gridDim.x), W), c = blockIdx.x;
             int64_t w = c < G ? c * W / G : 0;            // the next unit of this CTA, its end
             const int64_t w_end = c < G ? (c + 1) * W / G : 0;
@@ -379,7 +497,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     int64_t u = 0;
                     if (b0 + lane < p.batch) {
                         sequence(p, b0 + lane, a0, a1, a2, a3);
-                        u = head_units(TT, a1, a3) * p.Hkv;
+                        u = head_units(TT, a1, a3, extra) * p.Hkv;
                     }
                     int64_t incl = u;
 #pragma unroll
@@ -397,11 +515,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     before += __shfl_sync(0xffffffffu, incl, 31);
                 }
                 sequence(p, b, q0, nq, k0, nk);
-                const int64_t per_head = head_units(TT, nq, nk);
+                const int64_t per_head = head_units(TT, nq, nk, extra);
                 kvh = int(off / per_head);
                 off -= kvh * per_head;
                 for (;;) {
-                    const int u = max(1, tile_blocks(t0, TT, nq, nk));
+                    const int u = tile_units(tile_blocks(t0, TT, nq, nk), extra);
                     if (off < u)
                         break;
                     off -= u;
@@ -431,37 +549,39 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 return true;
             };
             for (; ok; ++it) {
-                const int islot = it % kItems;
-                if (!BL_WAIT(sm.item_empty[islot], (uint32_t(it / kItems) & 1u) ^ 1u))
-                    break;
+                // the next piece with work: blocks, or a tile without keys (its rows get zeros)
                 Item item = {};
-                if (w < w_end) {
-                    const int blocks = tile_blocks(t0, TT, nq, nk), units = max(1, blocks);
-                    const int take = int(min(int64_t(units) - off, w_end - w));
-                    item.valid = 1;
-                    item.kvh = kvh;
-                    item.q_row = q0 + t0;
-                    item.toks = min(TT, nq - t0);
-                    item.lim0 = int(max(int64_t(-0x40000000), int64_t(t0) + 1 + nk - nq));
-                    item.nk = nk;
-                    item.k_row = k0;
-                    item.j0 = int(off);
-                    item.n = blocks ? take : 0;
+                while (w < w_end && !item.valid) {
+                    const int blocks = tile_blocks(t0, TT, nq, nk), units = tile_units(blocks, extra);
+                    const int64_t take = min(units - off, w_end - w);
+                    const int j0 = unit_block(off, blocks, extra), j1 = unit_block(off + take, blocks, extra);
+                    if (j1 > j0 || (blocks == 0 && off == 0)) {
+                        item.valid = 1;
+                        item.kvh = kvh;
+                        item.q_row = q0 + t0;
+                        item.toks = min(TT, nq - t0);
+                        item.lim0 = int(max(int64_t(-0x40000000), int64_t(t0) + 1 + nk - nq));
+                        item.nk = nk;
+                        item.k_row = k0;
+                        item.j0 = j0;
+                        item.n = j1 - j0;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (PAIR) {
-                            const int rows = min(item.toks - s * p.TM, p.TM);
-                            const int kb = rows <= 0 ? 0 : tile_blocks(t0 + s * p.TM, rows, nq, nk);
-                            item.nb[s] = max(0, min(item.j0 + item.n, kb) - item.j0);
-                        } else {
-                            item.nb[s] = (item.n + 1 - s) / 2;
+                        for (int s = 0; s < 2; ++s) {
+                            if (PAIR) {
+                                const int rows = min(item.toks - s * p.TM, p.TM);
+                                const int kb = rows <= 0 ? 0 : tile_blocks(t0 + s * p.TM, rows, nq, nk);
+                                item.nb[s] = max(0, min(j1, kb) - j0);
+                            } else {
+                                item.nb[s] = (item.n + 1 - s) / 2;
+                            }
                         }
-                    }
-                    item.slot = take == units ? -1 : off ? 2 * int(c) : 2 * int(c) + 1;
-                    if (off == 0 && take < units && lane == 0) {
-                        // the CTA that holds unit w + units - 1
-                        const int64_t last = ((w + units) * G + W - 1) / W - 1;
-                        p.hdr[c] = JoinHeader{1, kvh, item.q_row, item.toks, int(last), {}};
+                        const bool begins = j0 == 0;
+                        item.slot = begins && j1 == blocks ? -1 : begins ? 2 * int(c) + 1 : 2 * int(c);
+                        if (begins && j1 < blocks && lane == 0) {
+                            // the CTA that holds the tile's last unit
+                            const int64_t last = ((w - off + units) * G + W - 1) / W - 1;
+                            p.hdr[c] = JoinHeader{1, kvh, item.q_row, item.toks, int(last), {}};
+                        }
                     }
                     w += take;
                     off += take;
@@ -481,6 +601,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         }
                     }
                 }
+                const int islot = it % kItems;
+                if (!BL_WAIT(sm.item_empty[islot], (uint32_t(it / kItems) & 1u) ^ 1u))
+                    break;
                 if (lane == 0) {
                     sm.item[islot] = item;
                     mbar_arrive(smem_u32(&sm.item_full[islot]));
@@ -560,12 +683,17 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             // O += P V of stream s; the products run in the order of their
             // issue, so the next scores may follow over P at once
             auto values = [&](int s, int x, bool first) {
+                const uint32_t d = tmem + uint32_t(256 + s * kHD), a = tmem + uint32_t(s * kKeys);
+                const uint64_t b = v_desc + uint64_t(x % kStages) * (kTile >> 4);
+                if (!BL_WAIT(sm.p_half[s], p_parity[s]))
+                    return false;
+                tc_fence_after();
+                mma_values(d, a, b, first ? 0u : 1u);
                 if (!BL_WAIT(sm.p_full[s], p_parity[s]))
                     return false;
-                p_parity[s] ^= 1u;
                 tc_fence_after();
-                mma_values(tmem + uint32_t(256 + s * kHD), tmem + uint32_t(s * kKeys),
-                           v_desc + uint64_t(x % kStages) * (kTile >> 4), first ? 0u : 1u);
+                mma_values(d, a + 32, b + 512, 1u);
+                p_parity[s] ^= 1u;
                 return true;
             };
             for (int it = 0; ok; ++it) {
@@ -799,10 +927,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 float mx[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    mx[x] = __uint_as_float(v[x]);
+                    mx[x] = fmaxf(__uint_as_float(v[x]), __uint_as_float(v[x + 4]));
 #pragma unroll
-                for (int x = 4; x < 128; ++x)
-                    mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(v[x]));
+                for (int x = 8; x < 128; x += 8)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        mx[y] = max3(mx[y], __uint_as_float(v[x + y]), __uint_as_float(v[x + y + 4]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (i == 0) {
                     m = top;
@@ -825,21 +955,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     }
                 }
                 const float mc = m == -INFINITY ? 0.0f : m * p.c;
-                float sum[4] = {};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const float a = exp2_approx(fmaf(__uint_as_float(v[64 * h + 2 * x]), p.c, -mc));
-                        const float b = exp2_approx(fmaf(__uint_as_float(v[64 * h + 2 * x + 1]), p.c, -mc));
-                        sum[x & 1] += a;
-                        sum[2 + (x & 1)] += b;
-                        w[x] = bf16x2(a, b);
-                    }
-                    tmem_st32_wait(s_tmem + uint32_t(32 * h), w);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const uint32_t half = smem_u32(&sm.p_half[s]);
+                l += j >= full ? row_weights<true>(v, p.c, mc, s_tmem, half)
+                               : row_weights<false>(v, p.c, mc, s_tmem, half);
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sm.p_full[s]));
             }
