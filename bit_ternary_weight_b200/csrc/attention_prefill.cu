@@ -37,7 +37,10 @@
 // Warp roles (384 threads; warp 11 idles):
 //   warps 0-3, 4-7  softmax of streams 0 and 1, a row per thread; epilogue
 //   warp 8          work list and TMA loads (Q, then K and V blocks in a ring)
-//   warp 9          MMA issue (lane 0, the whole warp in uniform control flow)
+//   warp 9          MMA issue (lane 0, the whole warp in uniform control flow),
+//                   the streams in turn: issued by a warp each, they drift
+//                   into step, and then both compute weights at once and both
+//                   wait for products at once (8192-token prompt 400 -> 440 us)
 //   warp 10         values behind a mask: in blocks where some row's keys are
 //                   masked, non-finite values of V are zeroed before the
 //                   product (a zero weight times a NaN would reach rows that
@@ -287,7 +290,7 @@ constexpr int kPoly = 4;
 
 template <bool MASKED>
 __device__ __forceinline__ float row_weights(const uint32_t (&v)[128], float c, float mc, uint32_t s_tmem,
-                                             uint32_t half)
+                                             uint32_t half, bool first_lane)
 {
     const uint64_t c2 = pack_f32x2(c, c), m2 = pack_f32x2(-mc, -mc);
     uint64_t sum[2] = {0, 0};       // two pairs of zeros
@@ -315,7 +318,9 @@ __device__ __forceinline__ float row_weights(const uint32_t (&v)[128], float c, 
     tmem_wait_st();
     tmem_keep32(w[0]);
     tc_fence_before();
-    mbar_arrive(half);
+    __syncwarp();
+    if (first_lane)
+        mbar_arrive(half);
 #pragma unroll
     for (int x = 40; x < 64; ++x)
         pair(x);
@@ -323,6 +328,20 @@ __device__ __forceinline__ float row_weights(const uint32_t (&v)[128], float c, 
     float s0, s1;
     unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
     return s0 + s1;
+}
+
+// Thirty-two bytes in one store where the address allows it: a row's stores
+// lie 32 lanes apart, and each costs a cache line per lane.
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8], bool aligned)
+{
+    if (aligned)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    else {
+        static_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 // ---------------------------------------------------------------- the work line
@@ -351,58 +370,105 @@ __device__ __forceinline__ int tile_blocks(int t0, int tt, int nq, int nk)
 // `extra` for what a tile costs besides (queries, epilogue).
 __device__ __forceinline__ int tile_units(int blocks, int extra) { return max(1, blocks) + extra; }
 
-// The block at unit x of a tile.  With 1 + extra units to a CTA or more, no
-// CTA's share of a tile is without a block.
+// The block at unit x of a tile: the extra units come first.  A CTA whose
+// share lies inside a tile has 1 + extra units of it or more (the shares are
+// never shorter where extra > 0), so it has a block.
 __device__ __forceinline__ int unit_block(int64_t x, int blocks, int extra)
 {
-    return int(x * blocks / tile_units(blocks, extra));
+    return int(max(int64_t(0), min(int64_t(blocks), x - extra)));
 }
 
-__device__ __forceinline__ int64_t head_units(int tt, int nq, int nk, int extra)
+// sum_{i < x} floor(i / 2^k)
+__device__ __forceinline__ int64_t shift_sum(int64_t x, int k)
 {
-    int64_t u = 0;
-    for (int64_t t0 = 0; t0 < nq; t0 += tt)
-        u += tile_units(tile_blocks(int(t0), tt, nq, nk), extra);
-    return u;
+    const int64_t q = x >> k;
+    return ((q * (q - 1) / 2) << k) + q * (x - (q << k));
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v)
+// sum_{i < n} floor((a i + b) / 128), a, b >= 0.  Multiples of 128 go to the
+// sum directly.  What is left of a, if a power of two, makes a sum of shifts;
+// else its terms step over at most a n / 128 multiples, and counting the i
+// behind each of them is the same sum with a and 128 swapped.
+__device__ __forceinline__ int64_t floor_sum128(int64_t n, int64_t a, int64_t b)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    int64_t sum = (a >> 7) * (n * (n - 1) / 2) + (b >> 7) * n;
+    a &= 127;
+    b &= 127;
+    if ((a & (a - 1)) == 0) {
+        const int k = a ? __ffs(int(a)) - 1 : 0;
+        return a ? sum + shift_sum(n + (b >> k), 7 - k) - shift_sum(b >> k, 7 - k) : sum;
+    }
+    for (int64_t m = 128; a * n + b >= m;) {
+        const int64_t top = a * n + b, t = m;
+        n = top / m;
+        b = top % m;
+        m = a;
+        a = t;
+        sum += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+        a %= m;
+        b %= m;
+    }
+    return sum;
+}
+
+// Units, without extra ones, of the `tiles` tiles of a head of a sequence.
+__device__ __forceinline__ int64_t head_units(int tt, int tiles, int nq, int nk)
+{
+    if (tiles == 0)
+        return 0;
+    const int64_t last = max(1, (nk + kKeys - 1) / kKeys);     // the last tile sees all keys
+    if (tiles == 1)
+        return last;
+    // tile i before it ends with the keys below base + (i + 1) tt: the first
+    // `blind` see none
+    const int64_t base = int64_t(nk) - nq;
+    const int64_t blind = base >= 0 ? 0 : min(tiles - 1, int(-base) / tt);
+    return blind + floor_sum128(tiles - 1 - blind, tt, base + (blind + 1) * tt + 127) + last;
 }
 
 // ---------------------------------------------------------------- kernel
 
-// mbar_wait without a call: a kernel that moves registers between its warps
-// (setmaxnreg) cannot hold one, since a callee's registers are not bounded.
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
-                                            uint64_t limit_ns = kWaitLimitNs)
+// mbar_wait of a whole warp.  All lanes try: with lane 0 alone (a predicated
+// try and a vote) an 8192-token prompt took 427 us instead of 357, with a
+// suspend-time hint 605.  Without a call: a kernel that moves registers between
+// its warps (setmaxnreg) cannot hold one, since a callee's registers are not
+// bounded.
+__device__ __forceinline__ bool try_wait_warp(uint32_t bar, uint32_t parity)
 {
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = global_timer_ns();
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+}
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                          uint64_t limit_ns = kWaitLimitNs)
+{
+    if (!try_wait_warp(bar, parity)) {
+        // the clock and the flag are read once in 64 tries: they would delay
+        // the next try, and most waits are part of a chain of hand-offs
+        uint64_t t0 = 0;
 #pragma unroll 1
-    for (;;) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if (abort_flag && *abort_flag)
-            return false;
-        if (global_timer_ns() - t0 > limit_ns) {
-            if (abort_flag)
-                *abort_flag = 1;
-            atomicExch(status, BL_ERR_TIMEOUT);
-            return false;
+        for (uint32_t tries = 1; !try_wait_warp(bar, parity); ++tries) {
+            if (tries % 64)
+                continue;
+            const uint64_t t = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+            if (!t0)
+                t0 = t;
+            if (__any_sync(0xffffffffu, abort_flag && *abort_flag))
+                return false;
+            if (t - t0 > limit_ns) {
+                if (abort_flag)
+                    *abort_flag = 1;
+                atomicExch(status, BL_ERR_TIMEOUT);
+                return false;
+            }
         }
     }
+    return true;
 }
 
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 
-// Waits that give up return false; a warp acts on its lanes' common outcome.
-#define BL_WAIT(bar, parity) __all_sync(0xffffffffu, wait_inline(smem_u32(&(bar)), (parity), abort_flag, p.status))
+// A warp's wait; false if it was given up (the same for every lane).
+#define BL_WAIT(bar, parity) wait_warp(smem_u32(&(bar)), (parity), abort_flag, p.status)
 
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -433,8 +499,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         mbar_init(smem_u32(&sm.q_empty), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sm.s_full[s]), 1);
-            mbar_init(smem_u32(&sm.p_half[s]), 128);
-            mbar_init(smem_u32(&sm.p_full[s]), 128);
+            mbar_init(smem_u32(&sm.p_half[s]), 4);          // a lane of each softmax warp
+            mbar_init(smem_u32(&sm.p_full[s]), 4);
             mbar_init(smem_u32(&sm.o_full[s]), 1);
         }
         mbar_init(smem_u32(&sm.ml_full), 128);
@@ -467,64 +533,97 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         if (warp == kLoadWarp) {
             // ---------------------------------------- work list, TMA loads
             const int TT = PAIR ? 2 * p.TM : p.TM;        // tokens of a tile
-            int64_t W = 0, tiles = 0;
-            bool bad = false;
-            for (int b0 = 0; b0 < p.batch; b0 += 32) {
-                int q0, nq = 0, k0, nk = 0;
-                if (b0 + lane < p.batch) {
-                    bad |= !sequence(p, b0 + lane, q0, nq, k0, nk);
-                    W += head_units(TT, nq, nk, 0);
-                    tiles += (nq + TT - 1) / TT;
-                }
-            }
-            W = warp_sum64(W) * p.Hkv;
-            tiles = warp_sum64(tiles) * p.Hkv;
-            if (bad && blockIdx.x == 0)
-                atomicExch(p.status, BL_ERR_SHAPE);
-            // short shares go by their blocks alone
-            const int extra = W >= 8 * int64_t(gridDim.x) ? kTileExtra : 0;
-            W += extra * tiles;
-            const int64_t G = min(int64_t(gridDim.x), W), c = blockIdx.x;
-            int64_t w = c < G ? c * W / G : 0;            // the next unit of this CTA, its end
-            const int64_t w_end = c < G ? (c + 1) * W / G : 0;
-            // the sequence that holds unit w
-            int b = 0, q0 = 0, nq = 0, k0 = 0, nk = 0, kvh = 0, t0 = 0;
-            int64_t off = w;                              // units from the tile's first to w
-            if (w < w_end) {
-                int64_t before = 0;
+            // lane l holds sequence chunk + l
+            int chunk = 0, l_q0 = 0, l_nq = 0, l_k0 = 0, l_nk = 0;
+            auto load_chunk = [&](int b0) {
+                chunk = b0;
+                l_nq = l_nk = 0;
+                return b0 + lane >= p.batch || sequence(p, b0 + lane, l_q0, l_nq, l_k0, l_nk);
+            };
+            // Two passes over the sequences, the first for the line's length:
+            // it holds sums of blocks and of tiles apart, since the cost of a
+            // tile beyond its blocks counts only where the shares are long.
+            // The code runs once, from a cold instruction cache, so it is kept
+            // small: no 64-bit division on the usual path.
+            int64_t W = 0, w = 0, w_end = 0, off = 0, c = blockIdx.x, G = 0;
+            int extra = 0, b = 0, q0 = 0, nq = 0, k0 = 0, nk = 0, kvh = 0, t0 = 0;
+            // floor(a / W) and floor(a / G)
+            auto over = [](int64_t a, int64_t d) {
+                return (uint64_t(a) | uint64_t(d)) >> 32 ? a / d : int64_t(uint32_t(a) / uint32_t(d));
+            };
+            auto take_sequence = [&](int next) {
+                b = next;
+                if (b < chunk || b >= chunk + 32)
+                    load_chunk(b & ~31);
+                q0 = __shfl_sync(0xffffffffu, l_q0, b - chunk);
+                nq = __shfl_sync(0xffffffffu, l_nq, b - chunk);
+                k0 = __shfl_sync(0xffffffffu, l_k0, b - chunk);
+                nk = __shfl_sync(0xffffffffu, l_nk, b - chunk);
+            };
+            bool fine = load_chunk(0);
+            for (int pass = 0; pass < 2; ++pass) {
+                int64_t before = 0, tiles = 0;
                 for (int b0 = 0; b0 < p.batch; b0 += 32) {
-                    int a0, a1 = 0, a2, a3 = 0;
-                    int64_t u = 0;
-                    if (b0 + lane < p.batch) {
-                        sequence(p, b0 + lane, a0, a1, a2, a3);
-                        u = head_units(TT, a1, a3, extra) * p.Hkv;
-                    }
+                    if (b0 != chunk)
+                        fine = load_chunk(b0) && fine;
+                    const int t = (l_nq + TT - 1) / TT;
+                    const int64_t u = head_units(TT, t, l_nq, l_nk) + extra * t;     // of one head
                     int64_t incl = u;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
                         incl += lane >= o ? v : 0;
                     }
-                    const unsigned past = __ballot_sync(0xffffffffu, before + incl > w);
-                    if (past) {
-                        const int l = __ffs(past) - 1;
-                        b = b0 + l;
-                        off = w - (before + __shfl_sync(0xffffffffu, incl - u, l));
-                        break;
+                    tiles += __reduce_add_sync(0xffffffffu, unsigned(t));
+                    if (pass) {
+                        const unsigned past = __ballot_sync(0xffffffffu, (before + incl) * p.Hkv > w);
+                        if (past) {
+                            const int l = __ffs(past) - 1;
+                            const int64_t per_head = __shfl_sync(0xffffffffu, u, l);
+                            off = w - (before + __shfl_sync(0xffffffffu, incl, l) - per_head) * p.Hkv;
+                            take_sequence(b0 + l);
+                            for (; off >= per_head; off -= per_head)
+                                ++kvh;
+                            break;
+                        }
                     }
                     before += __shfl_sync(0xffffffffu, incl, 31);
                 }
-                sequence(p, b, q0, nq, k0, nk);
-                const int64_t per_head = head_units(TT, nq, nk, extra);
-                kvh = int(off / per_head);
-                off -= kvh * per_head;
-                for (;;) {
-                    const int u = tile_units(tile_blocks(t0, TT, nq, nk), extra);
-                    if (off < u)
+                if (pass == 0) {
+                    W = before * p.Hkv;
+                    if (W >= 8 * int64_t(gridDim.x)) {
+                        extra = kTileExtra;
+                        W += extra * tiles * p.Hkv;
+                    }
+                    G = min(int64_t(gridDim.x), W);
+                    if (c < G) {
+                        w = over(c * W, G);
+                        w_end = over((c + 1) * W, G);
+                    }
+                    if (w == w_end)
                         break;
-                    off -= u;
-                    t0 += TT;
                 }
+            }
+            if (!fine && blockIdx.x == 0)
+                atomicExch(p.status, BL_ERR_SHAPE);
+            // the head's tile that holds unit off, 32 tiles at a time
+            while (w < w_end) {
+                const int64_t ti = int64_t(t0) + int64_t(lane) * TT;
+                int64_t u = ti < nq ? tile_units(tile_blocks(int(ti), TT, nq, nk), extra) : 0, incl = u;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                    incl += lane >= o ? v : 0;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, incl > off);
+                const int l = past ? __ffs(past) - 1 : 31;
+                if (past) {
+                    off -= __shfl_sync(0xffffffffu, incl - u, l);
+                    t0 += l * TT;
+                    break;
+                }
+                off -= __shfl_sync(0xffffffffu, incl, 31);
+                t0 += 32 * TT;
             }
             if (lane == 0)
                 p.hdr[c].valid = 0;
@@ -579,7 +678,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         item.slot = begins && j1 == blocks ? -1 : begins ? 2 * int(c) + 1 : 2 * int(c);
                         if (begins && j1 < blocks && lane == 0) {
                             // the CTA that holds the tile's last unit
-                            const int64_t last = ((w - off + units) * G + W - 1) / W - 1;
+                            const int64_t last = over((w - off + units) * G + W - 1, W) - 1;
                             p.hdr[c] = JoinHeader{1, kvh, item.q_row, item.toks, int(last), {}};
                         }
                     }
@@ -594,7 +693,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                                 kvh = 0;
                                 if (w < w_end) {
                                     do
-                                        sequence(p, ++b, q0, nq, k0, nk);
+                                        take_sequence(b + 1);
                                     while (nq == 0);
                                 }
                             }
@@ -659,10 +758,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             // copies in flight have landed before the CTA exits (at once
             // unless another role gave up before it took them)
             for (int x = max(0, loads - kStages); x < loads; ++x)
-                wait_inline(smem_u32(&sm.kv_full[x % kStages]), uint32_t(x / kStages) & 1u, nullptr, p.status,
+                wait_warp(smem_u32(&sm.kv_full[x % kStages]), uint32_t(x / kStages) & 1u, nullptr, p.status,
                             kDrainLimitNs);
             if (q_loads)
-                wait_inline(smem_u32(&sm.q_full), uint32_t(q_loads - 1) & 1u, nullptr, p.status, kDrainLimitNs);
+                wait_warp(smem_u32(&sm.q_full), uint32_t(q_loads - 1) & 1u, nullptr, p.status, kDrainLimitNs);
         } else if (warp == kMmaWarp) {
             // ---------------------------------------- MMA issue
             const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[0]));
@@ -680,8 +779,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                            k_desc + uint64_t(x % kStages) * (kTile >> 4));
                 mma_commit(smem_u32(&sm.s_full[s]));
             };
-            // O += P V of stream s; the products run in the order of their
-            // issue, so the next scores may follow over P at once
+            // O += P V of stream s, the first 64 keys while the others' weights
+            // are computed; the products run in the order of their issue, so
+            // the next scores may follow over P at once
             auto values = [&](int s, int x, bool first) {
                 const uint32_t d = tmem + uint32_t(256 + s * kHD), a = tmem + uint32_t(s * kKeys);
                 const uint64_t b = v_desc + uint64_t(x % kStages) * (kTile >> 4);
@@ -801,7 +901,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             if (issued) {
                 // every MMA has completed before tensor memory is released
                 mma_commit(smem_u32(&sm.drain));
-                wait_inline(smem_u32(&sm.drain), 0, nullptr, p.status, kDrainLimitNs);
+                wait_warp(smem_u32(&sm.drain), 0, nullptr, p.status, kDrainLimitNs);
             }
         } else if (warp == kFixWarp) {
             // ---------------------------------------- non-finite values behind masks
@@ -956,10 +1056,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 }
                 const float mc = m == -INFINITY ? 0.0f : m * p.c;
                 const uint32_t half = smem_u32(&sm.p_half[s]);
-                l += j >= full ? row_weights<true>(v, p.c, mc, s_tmem, half)
-                               : row_weights<false>(v, p.c, mc, s_tmem, half);
+                l += j >= full ? row_weights<true>(v, p.c, mc, s_tmem, half, lane == 0)
+                               : row_weights<false>(v, p.c, mc, s_tmem, half, lane == 0);
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sm.p_full[s]));
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm.p_full[s]));
             }
             if (!ok)
                 break;
@@ -999,6 +1101,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 }
                 const bool poisoned = *static_cast<volatile int *>(&sm.poison_piece) == it;
                 __nv_bfloat16 *dst = p.out + int64_t(item.q_row + tt) * p.o_row + int64_t(item.kvh * p.G + g) * p.o_head;
+                const bool aligned = reinterpret_cast<uintptr_t>(dst) % 32 == 0;
                 const int64_t prow = int64_t(item.slot) * (PAIR ? 2 * kRows : kRows) + s * kRows + r;
                 if (item.slot >= 0 && mine)
                     p.part_ml[prow] = make_float2(m, l);
@@ -1033,15 +1136,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                             continue;
                         if (item.slot < 0) {
 #pragma unroll
-                            for (int y = 0; y < 32; y += 8)
-                                *reinterpret_cast<uint4 *>(dst + x + y) =
-                                    make_uint4(bf16x2(a[y], a[y + 1]), bf16x2(a[y + 2], a[y + 3]),
-                                               bf16x2(a[y + 4], a[y + 5]), bf16x2(a[y + 6], a[y + 7]));
+                            for (int y = 0; y < 32; y += 16) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int z = 0; z < 8; ++z)
+                                    w[z] = bf16x2(a[y + 2 * z], a[y + 2 * z + 1]);
+                                store32(dst + x + y, w, aligned);
+                            }
                         } else {
 #pragma unroll
-                            for (int y = 0; y < 32; y += 4)
-                                *reinterpret_cast<float4 *>(p.part_o + prow * kHD + x + y) =
-                                    make_float4(a[y], a[y + 1], a[y + 2], a[y + 3]);
+                            for (int y = 0; y < 32; y += 8) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int z = 0; z < 8; ++z)
+                                    w[z] = __float_as_uint(a[y + z]);
+                                store32(p.part_o + prow * kHD + x + y, w, true);
+                            }
                         }
                     }
                 }
@@ -1209,7 +1319,7 @@ WsLayout ws_layout(int grid)
     WsLayout w{};
     w.ml = (size_t(grid) * sizeof(JoinHeader) + 127) / 128 * 128;
     w.o = w.ml + size_t(grid) * 2 * (2 * kRows) * sizeof(float2);
-    w.total = w.o + size_t(grid) * 2 * (2 * kRows) * kHD * sizeof(float);
+    w.total = w.o + size_t(grid) * 2 * (2 * kRows) * kHD * sizeof(float) + 128;    // base rounded up
     return w;
 }
 
@@ -1257,7 +1367,7 @@ int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s)
         return BL_ERR_CUDA;
     const int grid = main_grid(di), G = a.H / a.Hkv;
     const WsLayout w = ws_layout(grid);
-    auto *base = static_cast<unsigned char *>(a.ws);
+    auto *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(a.ws) + 127) / 128 * 128);
     PrefillParams p{};
     p.out = static_cast<__nv_bfloat16 *>(a.out.data);
     p.o_row = a.out.row_stride;
