@@ -38,9 +38,7 @@
 //   warps 0-3, 4-7  softmax of streams 0 and 1, a row per thread; epilogue
 //   warp 8          work list and TMA loads (Q, then K and V blocks in a ring)
 //   warp 9          MMA issue (lane 0, the whole warp in uniform control flow),
-//                   the streams in turn: issued by a warp each, they drift
-//                   into step, and then both compute weights at once and both
-//                   wait for products at once (8192-token prompt 400 -> 440 us)
+//                   the streams in turn
 //   warp 10         values behind a mask: in blocks where some row's keys are
 //                   masked, non-finite values of V are zeroed before the
 //                   product (a zero weight times a NaN would reach rows that
@@ -127,8 +125,7 @@ struct Smem {
     uint64_t v_fixed[kStages];
     uint64_t q_full, q_empty;
     uint64_t s_full[2];      // scores complete (and every earlier product)
-    uint64_t p_half[2];      // weights of the first 64 keys written over the scores
-    uint64_t p_full[2];      // all of them
+    uint64_t p_full[2];      // weights written over the scores
     uint64_t o_full[2];      // last product of the piece complete
     uint64_t ml_full;        // alt: stream 1's m and l are in ml
     uint64_t o1_read;        // alt: stream 1's O has been read
@@ -190,21 +187,26 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b)
         : "memory");
 }
 
-// Weights (tensor memory) times values: four MMAs over 64 keys, 16 keys (two
-// 8-row groups, 2048 bytes) each.
+// Weights (tensor memory) times values: eight MMAs over the 128 keys, 16 keys
+// (two 8-row groups, 2048 bytes) each.
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate)
 {
     asm volatile(
         "{\n\t.reg .pred e, p, t;\n\t.reg .b32 r;\n\t"
         "mov.u32 r, %%laneid;\n\t"
         "setp.eq.u32 e, r, 0;\n\t"
-        "setp.ne.b32 p, %10, 0;\n\t"
-        "setp.eq.b32 t, %10, %10;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n\t}" ::"r"(d),
-        "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b), "l"(b + 128), "l"(b + 256), "l"(b + 384),
+        "setp.ne.b32 p, %18, 0;\n\t"
+        "setp.eq.b32 t, %18, %18;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %9, %17, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %10, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %11, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %12, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %13, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%6], %14, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %15, %17, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%8], %16, %17, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "r"(a + 32), "r"(a + 40), "r"(a + 48), "r"(a + 56), "l"(b),
+        "l"(b + 128), "l"(b + 256), "l"(b + 384), "l"(b + 512), "l"(b + 640), "l"(b + 768), "l"(b + 896),
         "r"(kIdescPV), "r"(accumulate)
         : "memory");
 }
@@ -254,77 +256,34 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b)
     return d;
 }
 
-// 2^x of two values, -inf < x <= 127, on the FMA pipe: x = n + f with n the
-// nearest integer (adding 1.5 * 2^23 leaves it in the low bits), 2^f by the
-// cubic whose relative error on [-1/2, 1/2] is least (7.5e-5 = 2^-13.7, found
-// by linear programming on that error; bf16 weights round at 2^-9), and n
-// added to the exponent.  Below 2^-126 the result is some value under 2^-125.
-__device__ __forceinline__ void exp2_fma(uint64_t x, float &lo, float &hi)
-{
-    const uint64_t big = pack_f32x2(12582912.0f, 12582912.0f), neg = pack_f32x2(-12582912.0f, -12582912.0f);
-    float a, b;
-    unpack_f32x2(x, a, b);
-    x = pack_f32x2(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
-    const uint64_t n = add_f32x2(x, big);
-    const uint64_t f = fma_f32x2(add_f32x2(n, neg), pack_f32x2(-1.0f, -1.0f), x);
-    uint64_t p = fma_f32x2(f, pack_f32x2(0.0551716685295105f, 0.0551716685295105f),
-                           pack_f32x2(0.2426111251115799f, 0.2426111251115799f));
-    p = fma_f32x2(p, f, pack_f32x2(0.6932609677314758f, 0.6932609677314758f));
-    p = fma_f32x2(p, f, pack_f32x2(0.9999280571937561f, 0.9999280571937561f));
-    float pa, pb, na, nb;
-    unpack_f32x2(p, pa, pb);
-    unpack_f32x2(n, na, nb);
-    lo = __int_as_float(__float_as_int(pa) + (__float_as_int(na) << 23));
-    hi = __int_as_float(__float_as_int(pb) + (__float_as_int(nb) << 23));
-}
-
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// The weights of one row's scores, written over them as bf16: the first 64
-// keys' are handed on (`half`) while the others are computed.  Returns their
-// sum.  The exponentials are most of the work, and the unit that computes
-// them (4 a clock and quarter SM) would bind the kernel at the tensor cores'
-// own pace, so every kPoly-th pair goes to the FMA pipe instead; not in a
-// masked block, where a weight has to be zero exactly.
-constexpr int kPoly = 4;
-
-template <bool MASKED>
-__device__ __forceinline__ float row_weights(const uint32_t (&v)[128], float c, float mc, uint32_t s_tmem,
-                                             uint32_t half, bool first_lane)
+// The weights of one row's scores, written over them as bf16; returns their
+// sum.  Two exponentials, one packed multiply-add, one packed sum and one
+// conversion a pair: 128 exponentials take 1024 cycles of a quarter SM's unit
+// (4 a clock), about what the tensor cores need for the other stream.  A
+// cubic on the FMA pipe for every 4th pair took that unit's load down and the
+// 8192-token prompt from 343 to 363 us up: the issue slots are the scarcer.
+__device__ __forceinline__ float row_weights(const uint32_t (&v)[128], float c, float mc, uint32_t s_tmem)
 {
     const uint64_t c2 = pack_f32x2(c, c), m2 = pack_f32x2(-mc, -mc);
     uint64_t sum[2] = {0, 0};       // two pairs of zeros
     uint32_t w[2][32];
-    auto pair = [&](int x) {
-        const uint64_t t = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), c2, m2);
-        float a, b;
-        if (!MASKED && x % kPoly == kPoly - 1) {
-            exp2_fma(t, a, b);
-        } else {
-            unpack_f32x2(t, a, b);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+            const int e = 64 * h + 2 * x;
+            float a, b;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2, m2), a, b);
             a = exp2_approx(a);
             b = exp2_approx(b);
+            sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(a, b));
+            w[h][x] = bf16x2(a, b);
         }
-        sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(a, b));
-        w[x / 32][x % 32] = bf16x2(a, b);
-    };
-#pragma unroll
-    for (int x = 0; x < 32; ++x)
-        pair(x);
-    tmem_st32(s_tmem, w[0]);
-#pragma unroll
-    for (int x = 32; x < 40; ++x)
-        pair(x);
+        tmem_st32(s_tmem + uint32_t(32 * h), w[h]);
+    }
     tmem_wait_st();
     tmem_keep32(w[0]);
-    tc_fence_before();
-    __syncwarp();
-    if (first_lane)
-        mbar_arrive(half);
-#pragma unroll
-    for (int x = 40; x < 64; ++x)
-        pair(x);
-    tmem_st32_wait(s_tmem + 32, w[1]);
+    tmem_keep32(w[1]);
     float s0, s1;
     unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
     return s0 + s1;
@@ -499,8 +458,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         mbar_init(smem_u32(&sm.q_empty), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sm.s_full[s]), 1);
-            mbar_init(smem_u32(&sm.p_half[s]), 4);          // a lane of each softmax warp
-            mbar_init(smem_u32(&sm.p_full[s]), 4);
+            mbar_init(smem_u32(&sm.p_full[s]), 4);          // a lane of each softmax warp
             mbar_init(smem_u32(&sm.o_full[s]), 1);
         }
         mbar_init(smem_u32(&sm.ml_full), 128);
@@ -779,30 +737,37 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                            k_desc + uint64_t(x % kStages) * (kTile >> 4));
                 mma_commit(smem_u32(&sm.s_full[s]));
             };
-            // O += P V of stream s, the first 64 keys while the others' weights
-            // are computed; the products run in the order of their issue, so
-            // the next scores may follow over P at once
+            // O += P V of stream s (its weights are there); the products run in
+            // the order of their issue, so the next scores may follow over P
             auto values = [&](int s, int x, bool first) {
-                const uint32_t d = tmem + uint32_t(256 + s * kHD), a = tmem + uint32_t(s * kKeys);
-                const uint64_t b = v_desc + uint64_t(x % kStages) * (kTile >> 4);
-                if (!BL_WAIT(sm.p_half[s], p_parity[s]))
-                    return false;
-                tc_fence_after();
-                mma_values(d, a, b, first ? 0u : 1u);
-                if (!BL_WAIT(sm.p_full[s], p_parity[s]))
-                    return false;
-                tc_fence_after();
-                mma_values(d, a + 32, b + 512, 1u);
                 p_parity[s] ^= 1u;
-                return true;
+                tc_fence_after();
+                mma_values(tmem + uint32_t(256 + s * kHD), tmem + uint32_t(s * kKeys),
+                           v_desc + uint64_t(x % kStages) * (kTile >> 4), first ? 0u : 1u);
+            };
+            // A check costs this warp 150 to 200 cycles even where the phase
+            // is complete, and the tensor cores drain meanwhile, so the
+            // barriers of one step are tried together: V of load xv, K of load
+            // xk (-1: none) and the weights of stream s (-1: none).
+            auto ready = [&](int xv, int xk, int s) {
+                const uint32_t bv = smem_u32(&sm.kv_full[xv % kStages]), pv = uint32_t(xv / kStages) & 1u;
+                const uint32_t bk = xk < 0 ? bv : smem_u32(&sm.kv_full[xk % kStages]);
+                const uint32_t pk = xk < 0 ? pv : uint32_t(xk / kStages) & 1u;
+                const uint32_t bp = s < 0 ? bv : smem_u32(&sm.p_full[s]);
+                const uint32_t pp = s < 0 ? pv : s ? p_parity[1] : p_parity[0];
+                const bool v = mbar_try_wait(bv, pv), k = mbar_try_wait(bk, pk), w = mbar_try_wait(bp, pp);
+                if (__all_sync(0xffffffffu, v && k && w))
+                    return true;
+                return wait_warp(bv, pv, abort_flag, p.status) && wait_warp(bk, pk, abort_flag, p.status) &&
+                       wait_warp(bp, pp, abort_flag, p.status);
             };
             for (int it = 0; ok; ++it) {
                 const int islot = it % kItems;
                 if (!BL_WAIT(sm.item_full[islot], uint32_t(it / kItems) & 1u))
                     break;
-                const int valid = sm.item[islot].valid, n = sm.item[islot].n, j0 = sm.item[islot].j0;
+                const int valid = sm.item[islot].valid, n = sm.item[islot].n;
                 const int nb0 = sm.item[islot].nb[0], nb1 = sm.item[islot].nb[1];
-                const int full = max(0, min(sm.item[islot].nk, sm.item[islot].lim0)) / kKeys;
+                const int masked = max(0, min(sm.item[islot].nk, sm.item[islot].lim0)) / kKeys - sm.item[islot].j0;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sm.item_empty[islot]));
@@ -813,19 +778,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 if (!BL_WAIT(sm.q_full, uint32_t(q_loads) & 1u))
                     break;
                 ++q_loads;
-                issued = true;
-                // V of block i is complete, with non-finite values behind masks removed
-                auto v_ready = [&](int x, int i) {
-                    if (!landed(x))
+                issued = true;      // from here on commits are in flight, which the drain below outlasts
+                // non-finite values behind masks have been removed from V of block i, load x
+                auto fixed = [&](int x, int i) {
+                    if (i < masked)
+                        return true;
+                    const int st = x % kStages;
+                    if (!BL_WAIT(sm.v_fixed[st], (fixed_parity >> st) & 1u))
                         return false;
-                    if (j0 + i >= full) {
-                        const int st = x % kStages;
-                        if (!BL_WAIT(sm.v_fixed[st], (fixed_parity >> st) & 1u))
-                            return false;
-                        fixed_parity ^= 1u << st;
-                    }
+                    fixed_parity ^= 1u << st;
                     return true;
                 };
+                auto release = [&](int x) { mma_commit(smem_u32(&sm.kv_empty[x % kStages])); };
                 if (PAIR) {
                     if (!landed(loads))
                         break;
@@ -835,35 +799,34 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         scores(1, loads);
                     if (n == 1)
                         mma_commit(smem_u32(&sm.q_empty));
-                    mma_commit(smem_u32(&sm.kv_empty[loads % kStages]));
-                    for (int i = 0; i < n && ok; ++i) {
-                        const int xv = loads + 2 * i + 1, xk = xv + 1;
-                        ok = v_ready(xv, i);
-                        bool k_here = false;
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            const int nb = s ? nb1 : nb0;
-                            if (!ok || i >= nb)
-                                continue;
-                            ok = values(s, xv, i == 0);
-                            if (ok && i + 1 < nb) {
-                                ok = k_here || landed(xk);
-                                k_here = true;
-                                if (ok)
-                                    scores(s, xk);
-                            } else if (ok) {
-                                mma_commit(smem_u32(&sm.o_full[s]));
-                            }
-                        }
+                    release(loads);
+                    for (int i = 0; i < n; ++i) {
+                        const int xv = loads + 2 * i + 1, xk = i + 1 < n ? xv + 1 : -1;
+                        ok = ready(xv, xk, i < nb0 ? 0 : -1) && fixed(xv, i);
                         if (!ok)
                             break;
-                        mma_commit(smem_u32(&sm.kv_empty[xv % kStages]));
-                        if (i + 1 < n) {
-                            ok = k_here || landed(xk);
-                            mma_commit(smem_u32(&sm.kv_empty[xk % kStages]));
-                            if (i + 2 == n)
-                                mma_commit(smem_u32(&sm.q_empty));
+                        if (i < nb0) {
+                            values(0, xv, i == 0);
+                            if (i + 1 < nb0)
+                                scores(0, xk);
+                            else
+                                mma_commit(smem_u32(&sm.o_full[0]));
                         }
+                        if (i < nb1) {
+                            ok = BL_WAIT(sm.p_full[1], p_parity[1]);
+                            if (!ok)
+                                break;
+                            values(1, xv, i == 0);
+                            if (i + 1 < nb1)
+                                scores(1, xk);
+                            else
+                                mma_commit(smem_u32(&sm.o_full[1]));
+                        }
+                        release(xv);
+                        if (xk >= 0)
+                            release(xk);
+                        if (i + 2 == n)
+                            mma_commit(smem_u32(&sm.q_empty));
                     }
                 } else {
                     for (int i = 0; i < min(2, n) && ok; ++i) {
@@ -872,23 +835,27 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                             scores(i, loads + i);
                             if (i + 1 == n)
                                 mma_commit(smem_u32(&sm.q_empty));
-                            mma_commit(smem_u32(&sm.kv_empty[(loads + i) % kStages]));
+                            release(loads + i);
                         }
                     }
                     for (int i = 0; i < n && ok; ++i) {
+                        // the next K is not waited for here: where memory sets the
+                        // pace it arrives a block later
                         const int xv = loads + i + min(n, i + 2), s = i & 1;
-                        ok = v_ready(xv, i);
-                        if (ok)
-                            ok = s ? values(1, xv, i < 2) : values(0, xv, i < 2);
+                        ok = ready(xv, -1, s) && fixed(xv, i);
                         if (!ok)
                             break;
-                        mma_commit(smem_u32(&sm.kv_empty[xv % kStages]));
+                        if (s)
+                            values(1, xv, i < 2);
+                        else
+                            values(0, xv, i < 2);
+                        release(xv);
                         if (i + 2 < n) {
                             ok = landed(xv + 1);
                             if (!ok)
                                 break;
                             scores(s, xv + 1);
-                            mma_commit(smem_u32(&sm.kv_empty[(xv + 1) % kStages]));
+                            release(xv + 1);
                             if (i + 3 == n)
                                 mma_commit(smem_u32(&sm.q_empty));
                         } else {
@@ -1055,9 +1022,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     }
                 }
                 const float mc = m == -INFINITY ? 0.0f : m * p.c;
-                const uint32_t half = smem_u32(&sm.p_half[s]);
-                l += j >= full ? row_weights<true>(v, p.c, mc, s_tmem, half, lane == 0)
-                               : row_weights<false>(v, p.c, mc, s_tmem, half, lane == 0);
+                l += row_weights(v, p.c, mc, s_tmem);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
