@@ -95,8 +95,10 @@ template <int NT>
 __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const AdapterParams p)
 {
     __shared__ float red[kDownWarps / 2][kTile][NT * 8];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the second launch reads y before it waits for this one, so it may begin
+    // only when what came before this one is complete
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int64_t t0 = int64_t(blockIdx.x) * kTile;
     const int way = blockIdx.y, split = blockIdx.z;
@@ -122,30 +124,21 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
         };
         constexpr int kDeep = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;      // groups in flight
         const uint4 zero = make_uint4(0, 0, 0, 0);
-        int k = k0 + warp;
-        for (; k + (kDeep - 1) * kDownWarps < k1; k += kDeep * kDownWarps) {
+        for (int k = k0 + warp; k < k1; k += kDeep * kDownWarps) {
             uint4 xa[kDeep], xb[kDeep], b[kDeep][NT];
 #pragma unroll
             for (int s = 0; s < kDeep; ++s) {
                 const int64_t at = int64_t(k + s * kDownWarps) * 32;
-                xa[s] = r0 ? ld_dep_v4(x0 + at) : zero;
-                xb[s] = r1 ? ld_dep_v4(x1 + at) : zero;
+                const bool in = k + s * kDownWarps < k1;
+                xa[s] = in && r0 ? ld_dep_v4(x0 + at) : zero;
+                xb[s] = in && r1 ? ld_dep_v4(x1 + at) : zero;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    b[s][j] = j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
+                    b[s][j] = in && j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
             }
 #pragma unroll
             for (int s = 0; s < kDeep; ++s)
                 step(xa[s], xb[s], b[s]);
-        }
-        for (; k < k1; k += kDownWarps) {
-            uint4 b[NT];
-            const int64_t at = int64_t(k) * 32;
-            const uint4 xa = r0 ? ld_dep_v4(x0 + at) : zero, xb = r1 ? ld_dep_v4(x1 + at) : zero;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                b[j] = j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
-            step(xa, xb, b);
         }
         // sums of warps w and w + 4, then of the four pairs
         const int pair = warp & (kDownWarps / 2 - 1);
@@ -263,28 +256,56 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[TERMS
     }
 }
 
-// out = y + up u for one run of TILES tiles and the columns of a CTA.  A warp
-// has 32 columns; WAYS = 1: the warps of a CTA lie side by side and take the
-// tiles one after the other, every tile's y in flight from the start;
-// WAYS = 8: they share 32 columns and the adapters of one tile.  The tiles' u
-// come to shared memory first, the K splits' parts added in order.
+// out = y + up u for runs of tiles and the columns of a CTA.  A warp has 32
+// columns; WAYS = 1: the warps of a CTA lie side by side and take a run's
+// tiles one after the other, every tile's y in flight from the start; WAYS = 8:
+// they share 32 columns and the adapters of one tile.  y and the adapters are
+// asked for while the first launch still runs.  u, the K splits' parts added
+// in order, is split into its bf16 terms once per CTA, and a tile whose tokens
+// share one adapter (most tiles of a prompt) keeps its operand from tile to
+// tile and starts the accumulators at y (bf16 outputs; an fp32 output adds y at
+// the end, since a tensor core's sums lose up to 2^-23 of y each).
 template <int KB, bool F32, int WAYS>
-__global__ void __launch_bounds__(kUpWarps * 32) adapter_up_kernel(const AdapterParams p)
+__global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const AdapterParams p)
 {
     constexpr int kTiles = WAYS == 1 ? (F32 ? 2 : 4) : 1;
-    constexpr int kPitch = 16 * KB + 4;
-    __shared__ float u_s[kTiles * kTile][kPitch];
-    __shared__ int id_s[kTiles * kTile];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kTokens = kTiles * kTile;
+    constexpr int kTerms = F32 ? 3 : 2;
+    constexpr int kPitch = 8 * KB + 4;                        // words (two ranks) per token
+    __shared__ uint32_t u_s[kTerms][kTokens][kPitch];
+    __shared__ int id_s[kTokens];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int way = WAYS == 1 ? 0 : warp;
     const int64_t n0 = (int64_t(blockIdx.x) * (kUpWarps / WAYS) + (WAYS == 1 ? warp : 0)) * kUpCols;
     const int64_t nc = n0 + 8 * c;                            // this lane's output columns
     const bool cols = n0 < p.N;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int64_t run = blockIdx.y; run * kTiles * kTile < p.T; run += gridDim.y) {
-        const int64_t t0 = run * kTiles * kTile;
-        const int tokens = int(min(int64_t(kTiles * kTile), p.T - t0));
+    bool waited = false;
+    constexpr int kKept = KB <= 2 ? KB : 1;                   // k blocks of an adapter's operand in registers
+    uint2 b[kKept][4];
+    int b_of = -1;                                            // the adapter that b holds (KB <= 2)
+    auto load_kb = [&](int a, int kb, uint2 (&v)[4]) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            // column g of tile x: 8 (g / 2) + 2 x + g % 2; this lane's four ranks
+            const int64_t n = n0 + 8 * (g >> 1) + 2 * x + (g & 1);
+            const int k = 16 * kb + 4 * c;
+            v[x] = make_uint2(0, 0);
+            if (k < p.r && n < p.N)
+                v[x] = __ldg(reinterpret_cast<const uint2 *>(p.up + (int64_t(a) * p.N + n) * p.r + k));
+        }
+    };
+    auto load_b = [&](int a) {
+        if (KB > 2 || a == b_of)
+            return;
+        b_of = a;
+#pragma unroll
+        for (int kb = 0; kb < kKept; ++kb)
+            load_kb(a, kb, b[kb]);
+    };
+    for (int64_t run = blockIdx.y; run * kTokens < p.T; run += gridDim.y) {
+        const int64_t t0 = run * kTokens;
+        const int tokens = int(min(int64_t(kTokens), p.T - t0));
+        __syncthreads();                                      // the last run's u has been used
         Cols<F32> y[kTiles][2];
         if (cols) {
 #pragma unroll
@@ -294,21 +315,35 @@ __global__ void __launch_bounds__(kUpWarps * 32) adapter_up_kernel(const Adapter
                     if (16 * i + 8 * h + g < tokens)
                         y[i][h].load(p, t0 + 16 * i + 8 * h + g, nc);
         }
-        __syncthreads();                                      // the last run's u has been used
-        if (threadIdx.x < kTiles * kTile) {
-            int id = threadIdx.x < tokens ? int(ld_dep_u32(p.index + t0 + threadIdx.x)) : -1;
+        if (threadIdx.x < kTokens) {
+            const int id = int(threadIdx.x) < tokens ? int(ld_dep_u32(p.index + t0 + threadIdx.x)) : -1;
             id_s[threadIdx.x] = id < 0 || id >= p.n ? -1 : id;     // reported by the first launch
         }
-        for (int e = threadIdx.x; e < tokens * (p.r / 4); e += kUpWarps * 32) {
-            const int row = e / (p.r / 4), k = 4 * (e - row * (p.r / 4));
-            float4 s = {};
-            const float *u = p.u + (t0 + row) * p.r + k;
+        __syncthreads();
+        if (WAYS == 1 && cols && id_s[0] >= 0)
+            load_b(id_s[0]);
+        if (!waited) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            waited = true;
+        }
+        for (int e = threadIdx.x; e < tokens * 4 * KB; e += kUpWarps * 32) {
+            const int row = e / (4 * KB), k = 4 * (e % (4 * KB));
+            float4 s = {};                                    // ranks behind r are zeros
+            if (k < p.r && id_s[row] >= 0) {
+                const float *u = p.u + (t0 + row) * p.r + k;
 #pragma unroll 8
-            for (int z = 0; z < p.splits; ++z) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(u + int64_t(z) * p.T * p.r));
-                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+                for (int z = 0; z < p.splits; ++z) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(u + int64_t(z) * p.T * p.r));
+                    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+                }
             }
-            *reinterpret_cast<float4 *>(&u_s[row][k]) = s;
+            uint32_t lo[kTerms], hi[kTerms];
+            split_bf16(s.x, s.y, lo);
+            split_bf16(s.z, s.w, hi);
+#pragma unroll
+            for (int q = 0; q < kTerms; ++q)
+                *reinterpret_cast<uint2 *>(&u_s[q][row][k / 2]) = make_uint2(lo[q], hi[q]);
         }
         __syncthreads();
         if (!cols)
@@ -317,10 +352,56 @@ __global__ void __launch_bounds__(kUpWarps * 32) adapter_up_kernel(const Adapter
         for (int i = 0; i < kTiles; ++i) {
             if (16 * i >= tokens)
                 break;
-            const int id = lane < kTile ? id_s[16 * i + lane] : -1;
-            unsigned firsts = first_of(id, lane);
-            const unsigned none = __ballot_sync(0xffffffffu, lane < tokens - 16 * i && lane < kTile && id < 0);
             const int64_t ta = t0 + 16 * i + g, tb = ta + 8;
+            // acc += up u of adapter a for all 16 tokens (rows of other
+            // adapters are dropped by the caller)
+            auto product = [&](int a, float (&acc)[4][4]) {
+                load_b(a);
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (16 * kb >= p.r)
+                        break;
+                    if (KB > 2)
+                        load_kb(a, kb, b[0]);
+                    uint2 (&bk)[4] = b[KB > 2 ? 0 : kb];
+#pragma unroll
+                    for (int q = kTerms - 1; q >= 0; --q) {
+                        const uint2 ua = *reinterpret_cast<const uint2 *>(&u_s[q][16 * i + g][8 * kb + 2 * c]);
+                        const uint2 ub = *reinterpret_cast<const uint2 *>(&u_s[q][16 * i + g + 8][8 * kb + 2 * c]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma_bf16(acc[x], ua.x, ub.x, ua.y, ub.y, bk[x].x, bk[x].y);
+                    }
+                }
+            };
+            const int id = lane < kTile ? id_s[16 * i + lane] : -1;
+            const int valid = min(16, tokens - 16 * i), one = __shfl_sync(0xffffffffu, id, 0);
+            if (!F32 && WAYS == 1 && one >= 0 && __all_sync(0xffffffffu, id == one || lane >= valid)) {
+                float acc[4][4], f[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    y[i][h].floats(f);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        acc[x][2 * h] = f[2 * x];
+                        acc[x][2 * h + 1] = f[2 * x + 1];
+                    }
+                }
+                product(one, acc);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        f[2 * x] = acc[x][2 * h];
+                        f[2 * x + 1] = acc[x][2 * h + 1];
+                    }
+                    if (g + 8 * h < valid)
+                        store_cols<F32>(p, h ? tb : ta, nc, f);
+                }
+                continue;
+            }
+            unsigned firsts = first_of(id, lane);
+            const unsigned none = __ballot_sync(0xffffffffu, lane < valid && id < 0);
             if (way == 0) {                                   // tokens without an adapter
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -336,45 +417,11 @@ __global__ void __launch_bounds__(kUpWarps * 32) adapter_up_kernel(const Adapter
                     continue;
                 const int a = __shfl_sync(0xffffffffu, id, __ffs(firsts) - 1);
                 const unsigned rows = __ballot_sync(0xffffffffu, id == a);
-                const bool r0 = rows >> g & 1, r1 = rows >> (g + 8) & 1;
                 float acc[4][4] = {};
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    const int k = 16 * kb + 4 * c;            // this lane's four ranks
-                    if (16 * kb >= p.r)
-                        break;
-                    uint2 b[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        // column g of tile x: 8 (g / 2) + 2 x + g % 2
-                        const int64_t n = n0 + 8 * (g >> 1) + 2 * x + (g & 1);
-                        b[x] = make_uint2(0, 0);
-                        if (k < p.r && n < p.N)
-                            b[x] = __ldg(reinterpret_cast<const uint2 *>(p.up + (int64_t(a) * p.N + n) * p.r + k));
-                    }
-                    // rows of other adapters are dropped below; ranks behind r are zero
-                    float4 ua = {}, ub = {};
-                    if (k < p.r) {
-                        if (r0)
-                            ua = *reinterpret_cast<const float4 *>(&u_s[16 * i + g][k]);
-                        if (r1)
-                            ub = *reinterpret_cast<const float4 *>(&u_s[16 * i + g + 8][k]);
-                    }
-                    constexpr int kTerms = F32 ? 3 : 2;
-                    uint32_t w0[kTerms], w1[kTerms], w2[kTerms], w3[kTerms];
-                    split_bf16(ua.x, ua.y, w0);
-                    split_bf16(ub.x, ub.y, w1);
-                    split_bf16(ua.z, ua.w, w2);
-                    split_bf16(ub.z, ub.w, w3);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-#pragma unroll
-                        for (int s = kTerms - 1; s >= 0; --s)
-                            mma_bf16(acc[x], w0[s], w1[s], w2[s], w3[s], b[x].x, b[x].y);
-                }
+                product(a, acc);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (h ? r1 : r0) {
+                    if (rows >> (g + 8 * h) & 1) {
                         float f[8];
                         y[i][h].floats(f);
 #pragma unroll
@@ -390,13 +437,13 @@ __global__ void __launch_bounds__(kUpWarps * 32) adapter_up_kernel(const Adapter
     }
 }
 
-// K splits of the first launch: enough CTAs for the GPU while each warp still
-// has a 32-k group (K >= 64; T is all the workspace's size may depend on, so
+// K splits of the first launch: six CTAs per SM (a warp's groups are then in
+// flight at once) while each warp still has a 32-k group (K >= 64; T is all the workspace's size may depend on, so
 // the splits go by the tokens and the launch takes no more than K allows).
 int max_splits(int64_t T, int sms)
 {
     const int64_t tiles = (T + kTile - 1) / kTile;
-    return int(std::clamp<int64_t>(2 * sms / tiles, 1, 32));
+    return int(std::clamp<int64_t>(6 * sms / tiles, 1, 32));
 }
 
 cudaError_t launch(void (*kernel)(AdapterParams), dim3 grid, int threads, bool pdl, cudaStream_t s,

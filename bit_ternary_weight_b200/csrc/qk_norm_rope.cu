@@ -88,8 +88,8 @@ struct Raw8 {
 
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
-    return uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(a))) |
-           uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(b))) << 16;
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 __device__ __forceinline__ uint4 pack8(const float f[8])
@@ -106,9 +106,9 @@ __device__ __forceinline__ void rotate(float &a, float &b, float2 cs)
 }
 
 template <int XT, bool HALVES>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_kernel(const RopeParams p)
 {
-    constexpr int kAhead = XT == BL_BF16 ? 4 : 2;        // steps whose heads are in flight
+    constexpr int kAhead = XT == BL_BF16 ? 3 : 2;        // steps whose heads are in flight
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t item = (int64_t(blockIdx.x) * kRopeThreads + threadIdx.x) / 32;
@@ -148,6 +148,9 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         cs[i] = __ldg(tab + (HALVES ? 8 * c + i : i < 4 ? 4 * c + i : 32 + 4 * c + i - 4));
+    // gains of the kind of head (0: query, 1: key) that was taken last
+    float ga[8], gb[8];
+    int kind = -1;
     for (int h0 = first; h0 - lane / kHeadLanes < last; h0 += 4 * kAhead) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -170,16 +173,18 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
             if (h >= last || (!is_q && row < 0))
                 continue;
             if (gain) {
-                const float r = __fdiv_rn(1.0f, __fsqrt_rn(s * (1.0f / kHD) + p.eps));
-                float g[8];
-                gain8(gain, p.gt, 8 * c, g);
+                if (kind != int(is_k)) {
+                    kind = is_k;
+                    gain8(gain, p.gt, 8 * c, ga);
+                    gain8(gain, p.gt, 64 + 8 * c, gb);
+                }
+                // fp32 to 2^-22; the result rounds at 2^-8
+                const float r = rsqrtf(fmaf(s, 1.0f / kHD, p.eps));
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    a[i] = a[i] * r * g[i];
-                gain8(gain, p.gt, 64 + 8 * c, g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    b[i] = b[i] * r * g[i];
+                for (int i = 0; i < 8; ++i) {
+                    a[i] = a[i] * r * ga[i];
+                    b[i] = b[i] * r * gb[i];
+                }
             }
             if (is_q || is_k) {
                 if (HALVES) {
