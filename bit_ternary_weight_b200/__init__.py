@@ -25,6 +25,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -200,11 +201,16 @@ def _on(device: torch.device):
     return contextlib.nullcontext()
 
 
-def _call(fn, where: str, device: torch.device, args):
+def _elsewhere(device: torch.device) -> bool:
+    """Whether the tensors' GPU is another one than the current."""
+    return device.type == "cuda" and device.index not in (None, torch._C._cuda_getDevice())
+
+
+def _call(fn, where: str, device: torch.device, *args):
     """fn(*args, stream) on the tensors' GPU and its current stream.  Entering a
     device costs more host time than the rest of a short call, so it is done
     only where another one is current."""
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
+    if _elsewhere(device):
         with torch.cuda.device(device):
             status = fn(*args, _stream(device))
     else:
@@ -675,7 +681,7 @@ BL_FLAG_ROPE_HALVES = 8
 
 def _scratch(size, where: str, device: torch.device, *args) -> torch.Tensor:
     """Device memory of the bytes that the library's `size` function says."""
-    if device.type == "cuda" and device.index not in (None, torch.cuda.current_device()):
+    if _elsewhere(device):
         with torch.cuda.device(device):
             n = size(*args)
     else:
@@ -688,20 +694,22 @@ def _scratch(size, where: str, device: torch.device, *args) -> torch.Tensor:
 def _heads(t, where: str, name: str, dtypes, heads, rows):
     """The rows of heads [rows][heads][128] of a tensor (None: any number), as
     the four numbers of a HeadsC."""
-    shape, stride = t.shape, t.stride()
+    try:
+        n, h, d = t.shape
+        row, head, one = t.stride()
+    except ValueError:
+        d = 0
     if t.dtype not in dtypes:
         want = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise BitLinearError(BL_ERR_DTYPE, where,
                              f"{name} is {str(t.dtype).replace('torch.', '')}, needs {want}")
-    if len(shape) != 3 or shape[2] != 128 or stride[2] != 1 or \
-            (heads is not None and shape[1] != heads) or (rows is not None and shape[0] != rows):
+    if d != 128 or one != 1 or (heads is not None and h != heads) or (rows is not None and n != rows):
         raise BitLinearError(
-            BL_ERR_SHAPE, where, f"{name} of shape {tuple(shape)} and strides {stride} is not "
+            BL_ERR_SHAPE, where, f"{name} of shape {tuple(t.shape)} and strides {t.stride()} is not "
             f"[{'rows' if rows is None else rows}][{'heads' if heads is None else heads}][128]")
-    return t.data_ptr(), shape[0], stride[0], stride[1]
+    return t.data_ptr(), n, row, head
 
 
-_HeadsArray = {n: ctypes.c_int64 * (4 * n) for n in (4, 6)}
 _NO_HEADS = (0, 0, 0, 0)
 
 
@@ -730,10 +738,11 @@ def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float
     may be its own input, in place.
     """
     where = "bitlinear_qk_norm_rope"
-    if q.dim() != 3 or k.dim() != 3:
-        raise BitLinearError(BL_ERR_SHAPE, where, f"q of shape {tuple(q.shape)}, k of shape {tuple(k.shape)}")
-    T, H, _ = q.shape
-    Hkv = k.shape[1]
+    dims, kdims = q.shape, k.shape
+    if len(dims) != 3 or len(kdims) != 3:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"q of shape {tuple(dims)}, k of shape {tuple(kdims)}")
+    T, H, _ = dims
+    Hkv = kdims[1]
     dtype, device = q.dtype, q.device
     if k.dtype != dtype or (v is not None and v.dtype != dtype):
         raise BitLinearError(BL_ERR_DTYPE, where, "q, k and v of mixed element types")
@@ -747,11 +756,11 @@ def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float
     if v is not None and v_out is None:
         v_out = torch.empty(T, Hkv, 128, dtype=torch.bfloat16, device=device)
     ko = _heads(k_out, where, "k_out", _BF16, Hkv, None)
-    arr = _HeadsArray[6](
+    arr = array("q", (
         *_heads(q, where, "q", _FLOATS, H, T), *_heads(k, where, "k", _FLOATS, Hkv, T),
         *(_NO_HEADS if v is None else _heads(v, where, "v", _FLOATS, Hkv, T)),
         *_heads(q_out, where, "q_out", _BF16, H, T), *ko,
-        *(_NO_HEADS if v is None else _heads(v_out, where, "v_out", _BF16, Hkv, ko[1])))
+        *(_NO_HEADS if v is None else _heads(v_out, where, "v_out", _BF16, Hkv, ko[1]))))
     if slots is None and ko[1] < T:
         raise BitLinearError(BL_ERR_SHAPE, where, f"k_out has {ko[1]} rows for {T} tokens")
     rows = table.shape
@@ -765,12 +774,12 @@ def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float
             gt = _dt(g.dtype)
     if q_gain is not None and k_gain is not None and q_gain.dtype != k_gain.dtype:
         raise BitLinearError(BL_ERR_DTYPE, where, "gains of mixed element types")
-    at = ctypes.addressof(arr)
+    at = arr.buffer_info()[0]
     flags = (BL_FLAG_PDL if pdl else 0) | (BL_FLAG_ROPE_HALVES if halves else 0)
-    _call(_lib.bitlinear_qk_norm_rope, where, device, (
+    _call(_lib.bitlinear_qk_norm_rope, where, device,
         at, at + 32, at + 64, _dt(dtype), H, Hkv, 128, _vector(positions, where, "positions", _I32, T),
         _vector(table, where, "table", _F32, rows[0] * 128), rows[0], gains[0], gains[1], gt, eps,
-        None if slots is None else _vector(slots, where, "slots", _I32, T), at + 96, at + 128, at + 160, flags))
+        None if slots is None else _vector(slots, where, "slots", _I32, T), at + 96, at + 128, at + 160, flags)
     return q_out, k_out, v_out
 
 
@@ -796,15 +805,16 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=
     outside every sequence stay as they were.
     """
     where = "bitlinear_attention_prefill"
-    if q.dim() != 3 or k.dim() != 3:
-        raise BitLinearError(BL_ERR_SHAPE, where, f"q of shape {tuple(q.shape)}, k of shape {tuple(k.shape)}")
+    dims, kdims = q.shape, k.shape
+    if len(dims) != 3 or len(kdims) != 3:
+        raise BitLinearError(BL_ERR_SHAPE, where, f"q of shape {tuple(dims)}, k of shape {tuple(kdims)}")
     device = q.device
     if cu_k is None:
         cu_k = cu_q
     if out is None:
         out = torch.zeros(q.shape, dtype=torch.bfloat16, device=device)
-    T, H, _ = q.shape
-    Hkv = k.shape[1]
+    T, H, _ = dims
+    Hkv = kdims[1]
     if Hkv < 1 or H % Hkv:
         raise BitLinearError(BL_ERR_SHAPE, where, f"{H} query heads for {Hkv} kv heads")
     batch = cu_q.numel() - 1
@@ -812,15 +822,15 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=
     if cu_k.numel() != batch + 1:
         raise BitLinearError(BL_ERR_SHAPE, where, f"cu_q of {batch + 1} bounds, cu_k of {cu_k.numel()}")
     kh = _heads(k, where, "k", _BF16, None, None)
-    arr = _HeadsArray[4](*_heads(q, where, "q", _BF16, None, None), *kh, *_heads(v, where, "v", _BF16, Hkv, kh[1]),
-                         *_heads(out, where, "out", _BF16, H, T))
+    arr = array("q", (*_heads(q, where, "q", _BF16, None, None), *kh, *_heads(v, where, "v", _BF16, Hkv, kh[1]),
+                      *_heads(out, where, "out", _BF16, H, T)))
     if workspace is None:
         workspace = attention_prefill_workspace(H, Hkv, device)
     ws = _vector(workspace, where, "workspace", (workspace.dtype,), 1)
-    at = ctypes.addressof(arr)
-    _call(_lib.bitlinear_attention_prefill, where, device, (
+    at = arr.buffer_info()[0]
+    _call(_lib.bitlinear_attention_prefill, where, device,
         at, at + 32, at + 64, *bounds, batch, H, Hkv, 128, 128 ** -0.5 if scale is None else scale, at + 96, ws,
-        workspace.nbytes, BL_FLAG_PDL if pdl else 0))
+        workspace.nbytes, BL_FLAG_PDL if pdl else 0)
     return out
 
 
@@ -869,11 +879,11 @@ def adapter_add(y, x, down, up, index, scale=None, out=None, workspace=None, pdl
     ldo = _rows(out, where, "out", _FLOATS, T, N)
     if workspace is None:
         workspace = adapter_workspace(T, r, device)
-    _call(_lib.bitlinear_adapter_add, where, device, (
+    _call(_lib.bitlinear_adapter_add, where, device,
         y.data_ptr(), _dt(y.dtype), ldy, x.data_ptr(), ldx, T, N, K, _vector(down, where, "down", _BF16, n * r * K),
         _vector(up, where, "up", _BF16, n * N * r), n, r, _vector(index, where, "index", _I32, T),
         None if scale is None else _vector(scale, where, "scale", _F32, n), out.data_ptr(), ldo,
-        _vector(workspace, where, "workspace", (workspace.dtype,), 1), workspace.nbytes, BL_FLAG_PDL if pdl else 0))
+        _vector(workspace, where, "workspace", (workspace.dtype,), 1), workspace.nbytes, BL_FLAG_PDL if pdl else 0)
     return out
 
 
