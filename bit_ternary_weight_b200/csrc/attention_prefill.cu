@@ -147,11 +147,12 @@ static_assert(smem_bytes<true>() > 114 * 1024 && smem_bytes<false>() > 114 * 102
 
 // ---------------------------------------------------------------- PTX wrappers
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2)
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
 }
 
@@ -519,33 +520,42 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 nk = __shfl_sync(0xffffffffu, l_nk, b - chunk);
             };
             bool fine = load_chunk(0);
+            int64_t u = 0, incl = 0;     // units without extra ones of a head of lane's sequence; of the chunk's up to it
+            int t = 0, tin = 0;          // the same of tiles
             for (int pass = 0; pass < 2; ++pass) {
                 int64_t before = 0, tiles = 0;
                 for (int b0 = 0; b0 < p.batch; b0 += 32) {
                     if (b0 != chunk)
                         fine = load_chunk(b0) && fine;
-                    const int t = (l_nq + TT - 1) / TT;
-                    const int64_t u = head_units(TT, t, l_nq, l_nk) + extra * t;     // of one head
-                    int64_t incl = u;
+                    if (pass == 0 || p.batch > 32) {
+                        t = tin = (l_nq + TT - 1) / TT;
+                        u = incl = head_units(TT, t, l_nq, l_nk);
+                        if (p.batch > 1) {
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                        incl += lane >= o ? v : 0;
+                            for (int o = 1; o < 32; o <<= 1) {
+                                const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                                const int z = __shfl_up_sync(0xffffffffu, tin, o);
+                                incl += lane >= o ? v : 0;
+                                tin += lane >= o ? z : 0;
+                            }
+                        }
                     }
-                    tiles += __reduce_add_sync(0xffffffffu, unsigned(t));
                     if (pass) {
-                        const unsigned past = __ballot_sync(0xffffffffu, (before + incl) * p.Hkv > w);
+                        const int64_t upto = before + incl + int64_t(extra) * tin;
+                        const unsigned past = __ballot_sync(0xffffffffu, upto * p.Hkv > w);
                         if (past) {
                             const int l = __ffs(past) - 1;
-                            const int64_t per_head = __shfl_sync(0xffffffffu, u, l);
-                            off = w - (before + __shfl_sync(0xffffffffu, incl, l) - per_head) * p.Hkv;
+                            const int64_t per_head = __shfl_sync(0xffffffffu, u + int64_t(extra) * t, l);
+                            off = w - (__shfl_sync(0xffffffffu, upto, l) - per_head) * p.Hkv;
                             take_sequence(b0 + l);
                             for (; off >= per_head; off -= per_head)
                                 ++kvh;
                             break;
                         }
                     }
-                    before += __shfl_sync(0xffffffffu, incl, 31);
+                    const int end = p.batch > 1 ? 31 : 0;
+                    before += __shfl_sync(0xffffffffu, incl + int64_t(extra) * tin, end);
+                    tiles += __shfl_sync(0xffffffffu, tin, end);
                 }
                 if (pass == 0) {
                     W = before * p.Hkv;
@@ -565,22 +575,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             if (!fine && blockIdx.x == 0)
                 atomicExch(p.status, BL_ERR_SHAPE);
             // the head's tile that holds unit off, 32 tiles at a time
-            while (w < w_end) {
+            while (w < w_end && nq > TT) {
                 const int64_t ti = int64_t(t0) + int64_t(lane) * TT;
-                int64_t u = ti < nq ? tile_units(tile_blocks(int(ti), TT, nq, nk), extra) : 0, incl = u;
+                const int64_t len = ti < nq ? tile_units(tile_blocks(int(ti), TT, nq, nk), extra) : 0;
+                int64_t upto = len;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                    incl += lane >= o ? v : 0;
+                    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                    upto += lane >= o ? v : 0;
                 }
-                const unsigned past = __ballot_sync(0xffffffffu, incl > off);
-                const int l = past ? __ffs(past) - 1 : 31;
+                const unsigned past = __ballot_sync(0xffffffffu, upto > off);
                 if (past) {
-                    off -= __shfl_sync(0xffffffffu, incl - u, l);
+                    const int l = __ffs(past) - 1;
+                    off -= __shfl_sync(0xffffffffu, upto - len, l);
                     t0 += l * TT;
                     break;
                 }
-                off -= __shfl_sync(0xffffffffu, incl, 31);
+                off -= __shfl_sync(0xffffffffu, upto, 31);
                 t0 += 32 * TT;
             }
             if (lane == 0)
@@ -598,8 +609,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     mbar_arrive_tx(bar, uint32_t(qt * p.TM * p.G) * 256u);
                     for (int s = 0; s < qt; ++s) {
                         const uint32_t dst = smem_u32(sm.q[s]);
-                        tma_load_3d(dst, &qmap, bar, 0, item.kvh * p.G, item.q_row + s * p.TM);
-                        tma_load_3d(dst + kBox, &qmap, bar, 64, item.kvh * p.G, item.q_row + s * p.TM);
+                        tma_load_4d(dst, &qmap, bar, 0, item.kvh * p.G, item.q_row + s * p.TM, 0);
+                        tma_load_4d(dst + kBox, &qmap, bar, 0, item.kvh * p.G, item.q_row + s * p.TM, 1);
                     }
                 }
                 __syncwarp();
@@ -676,7 +687,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 // piece is complete: their stages come free without these
                 // queries, so the ring never waits for itself.
                 const int n = item.n, masked = max(0, min(item.nk, item.lim0)) / kKeys - item.j0;
-                const int early = min(2 * n, kStages - 2);
+                // (the first piece's queries come first: their place is free)
+                const int early = q_loads ? min(2 * n, kStages - 2) : 0;
                 for (int x = 0; x < 2 * n && ok; ++x, ++loads) {
                     if (x == early)
                         ok = load_q(item);
@@ -695,7 +707,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         i = y > 2 * (n - 2) ? y - max(0, n - 2) : is_v ? y / 2 : y / 2 + 2;
                     }
                     const int st = loads % kStages;
-                    ok = ok && BL_WAIT(sm.kv_empty[st], (uint32_t(loads / kStages) & 1u) ^ 1u);
+                    ok = ok && (loads < kStages || BL_WAIT(sm.kv_empty[st], (uint32_t(loads / kStages) & 1u) ^ 1u));
                     if (!ok)
                         break;
                     if (lane == 0) {
@@ -703,14 +715,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         const CUtensorMap *map = is_v ? &vmap : &kmap;
                         const int row = item.k_row + (item.j0 + i) * kKeys;
                         mbar_arrive_tx(bar, kTile);
-                        tma_load_3d(dst, map, bar, 0, item.kvh, row);
-                        tma_load_3d(dst + kBox, map, bar, 64, item.kvh, row);
+                        tma_load_4d(dst, map, bar, 0, item.kvh, row, 0);
                         if (is_v && i >= masked)
                             mbar_arrive(smem_u32(&sm.v_posted[st]));
                     }
                     __syncwarp();
                 }
-                if (ok && early == 2 * n)
+                if (ok && early == 2 * n)       // all of them
                     ok = load_q(item);
             }
             // copies in flight have landed before the CTA exits (at once
@@ -1256,17 +1267,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// [rows][heads][128] bf16 as a 3-D map, boxes of 64 values x box_heads x box_rows.
-int make_map(CUtensorMap *map, const bitlinear_heads &h, int heads, uint32_t box_heads, uint32_t box_rows)
+// [rows][heads][128] bf16 as a 4-D map of 64 values x heads x rows x 2 halves
+// of the head: a box of both halves is the two swizzle-wide columns of an
+// operand tile, one behind the other, in one copy.
+int make_map(CUtensorMap *map, const bitlinear_heads &h, int heads, uint32_t box_heads, uint32_t box_rows,
+             uint32_t box_halves)
 {
     auto fn = encode_fn();
     if (!fn)
         return BL_ERR_CUDA;
-    const cuuint64_t dims[3] = {kHD, cuuint64_t(heads), cuuint64_t(h.rows)};
-    const cuuint64_t strides[2] = {cuuint64_t(heads == 1 ? kHD : h.head_stride) * 2,
-                                   cuuint64_t(h.rows == 1 ? kHD : h.row_stride) * 2};
-    const cuuint32_t box[3] = {64, box_heads, box_rows}, estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, h.data, dims, strides, box, estr,
+    const cuuint64_t dims[4] = {kHD / 2, cuuint64_t(heads), cuuint64_t(h.rows), 2};
+    const cuuint64_t strides[3] = {cuuint64_t(heads == 1 ? kHD : h.head_stride) * 2,
+                                   cuuint64_t(h.rows == 1 ? kHD : h.row_stride) * 2, kHD};
+    const cuuint32_t box[4] = {kHD / 2, box_heads, box_rows, box_halves}, estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, h.data, dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? BL_OK : BL_ERR_CUDA;
@@ -1352,8 +1366,9 @@ int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s)
     p.status = di->status;
     CUtensorMap qm, km, vm;
     int st;
-    if ((st = make_map(&qm, a.q, a.H, uint32_t(G), uint32_t(p.TM))) ||
-        (st = make_map(&km, a.k, a.Hkv, 1, kKeys)) || (st = make_map(&vm, a.v, a.Hkv, 1, kKeys)))
+    // (a tile of queries has TM * G rows, so its halves are copied apart)
+    if ((st = make_map(&qm, a.q, a.H, uint32_t(G), uint32_t(p.TM), 1)) ||
+        (st = make_map(&km, a.k, a.Hkv, 1, kKeys, 2)) || (st = make_map(&vm, a.v, a.Hkv, 1, kKeys, 2)))
         return st;
     // two tiles of rows per CTA once every CTA could have a pair of them
     const int64_t pairs = int64_t(a.Hkv) * (p.Tq / (2 * p.TM));
