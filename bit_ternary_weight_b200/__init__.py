@@ -721,8 +721,7 @@ def _vector(t, where: str, name: str, dtypes, n: int):
 
 
 def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float = RMS_EPS,
-                 slots=None, q_out=None, k_out=None, v_out=None, halves: bool = False,
-                 pdl: bool = False):
+                 slots=None, q_out=None, k_out=None, v_out=None, halves: bool = False):
     """Queries and keys of T tokens in one pass: RMS norm of each head (with
     q_gain / k_gain [128]; none without), rotation by the token's position, keys
     and values written to their cache rows.  Returns (q_out, k_out, v_out).
@@ -775,7 +774,7 @@ def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float
     if q_gain is not None and k_gain is not None and q_gain.dtype != k_gain.dtype:
         raise BitLinearError(BL_ERR_DTYPE, where, "gains of mixed element types")
     at = arr.buffer_info()[0]
-    flags = (BL_FLAG_PDL if pdl else 0) | (BL_FLAG_ROPE_HALVES if halves else 0)
+    flags = BL_FLAG_ROPE_HALVES if halves else 0
     _call(_lib.bitlinear_qk_norm_rope, where, device,
         at, at + 32, at + 64, _dt(dtype), H, Hkv, 128, _vector(positions, where, "positions", _I32, T),
         _vector(table, where, "table", _F32, rows[0] * 128), rows[0], gains[0], gains[1], gt, eps,
@@ -791,7 +790,7 @@ def attention_prefill_workspace(H: int, Hkv: int, device) -> torch.Tensor:
 
 
 def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=None,
-                      workspace=None, pdl: bool = False):
+                      workspace=None):
     """Causal attention of packed sequences with grouped heads.
 
     q [Tq, H, 128], k and v [Tk, Hkv, 128], bf16, any row and head strides (a
@@ -830,7 +829,7 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=
     at = arr.buffer_info()[0]
     _call(_lib.bitlinear_attention_prefill, where, device,
         at, at + 32, at + 64, *bounds, batch, H, Hkv, 128, 128 ** -0.5 if scale is None else scale, at + 96, ws,
-        workspace.nbytes, BL_FLAG_PDL if pdl else 0)
+        workspace.nbytes, 0)
     return out
 
 
@@ -852,7 +851,7 @@ def _rows(t, where: str, name: str, dtypes, rows: int, cols: int) -> int:
     return stride[0] if rows > 1 else cols
 
 
-def adapter_add(y, x, down, up, index, scale=None, out=None, workspace=None, pdl: bool = False):
+def adapter_add(y, x, down, up, index, scale=None, out=None, workspace=None):
     """Low-rank adapters of many requests beside one shared projection:
     out[t] = y[t] + scale[a] * up[a] @ (down[a] @ x[t]) with a = index[t], and
     out[t] = y[t] where index[t] is negative.
@@ -883,7 +882,7 @@ def adapter_add(y, x, down, up, index, scale=None, out=None, workspace=None, pdl
         y.data_ptr(), _dt(y.dtype), ldy, x.data_ptr(), ldx, T, N, K, _vector(down, where, "down", _BF16, n * r * K),
         _vector(up, where, "up", _BF16, n * N * r), n, r, _vector(index, where, "index", _I32, T),
         None if scale is None else _vector(scale, where, "scale", _F32, n), out.data_ptr(), ldo,
-        _vector(workspace, where, "workspace", (workspace.dtype,), 1), workspace.nbytes, BL_FLAG_PDL if pdl else 0)
+        _vector(workspace, where, "workspace", (workspace.dtype,), 1), workspace.nbytes, 0)
     return out
 
 

@@ -446,8 +446,7 @@ int max_splits(int64_t T, int sms)
     return int(std::clamp<int64_t>(6 * sms / tiles, 1, 32));
 }
 
-cudaError_t launch(void (*kernel)(AdapterParams), dim3 grid, int threads, bool pdl, cudaStream_t s,
-                   const AdapterParams &p)
+cudaError_t launch(void (*kernel)(AdapterParams), dim3 grid, int threads, cudaStream_t s, const AdapterParams &p)
 {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -457,7 +456,7 @@ cudaError_t launch(void (*kernel)(AdapterParams), dim3 grid, int threads, bool p
     cfg.blockDim = dim3(unsigned(threads));
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = 1;       // each kernel waits itself for what came before it
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -514,7 +513,7 @@ int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
                 : a.r <= 64 ? adapter_down_kernel<8>
                             : adapter_down_kernel<16>;
     const dim3 dgrid(unsigned(tiles), unsigned(p.down_ways), unsigned(p.splits));
-    int st = cuda_status(launch(down, dgrid, kDownWarps * 32, a.flags & BL_FLAG_PDL, s, p));
+    int st = cuda_status(launch(down, dgrid, kDownWarps * 32, s, p));
     if (st)
         return st;
     // few tokens: a CTA per 32 columns and 16 tokens, its warps share the adapters
@@ -523,7 +522,7 @@ int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
     const int64_t gx = (a.N + cols - 1) / cols, gy = (a.T + tokens - 1) / tokens;
     auto up = a.yt == BL_F32 ? (few ? up_kernel<true, 8>(a.r) : up_kernel<true, 1>(a.r))
                              : (few ? up_kernel<false, 8>(a.r) : up_kernel<false, 1>(a.r));
-    return cuda_status(launch(up, dim3(unsigned(gx), unsigned(std::min<int64_t>(gy, 65535))), kUpWarps * 32, true, s, p));
+    return cuda_status(launch(up, dim3(unsigned(gx), unsigned(std::min<int64_t>(gy, 65535))), kUpWarps * 32, s, p));
 }
 
 }  // namespace bl

@@ -674,7 +674,7 @@ int bitlinear_qk_norm_rope(const bitlinear_heads *q, const bitlinear_heads *k, c
     if (!valid_dtype(xt) || ((q_gain || k_gain) && !valid_dtype(gt)))
         return BL_ERR_DTYPE;
     if (D != 128 || H < 1 || Hkv < 1 || H > 1024 || Hkv > 1024 || table_rows < 1 ||
-        table_rows > (int64_t(1) << 31) || (flags & ~(BL_FLAG_PDL | BL_FLAG_ROPE_HALVES)) ||
+        table_rows > (int64_t(1) << 31) || (flags & ~BL_FLAG_ROPE_HALVES) ||
         ((q_gain || k_gain) && (!(eps >= 0.0f) || !(eps <= 3.0e38f))))
         return BL_ERR_SHAPE;
     const int64_t T = q->rows;
@@ -748,7 +748,7 @@ int bitlinear_attention_prefill(const bitlinear_heads *q, const bitlinear_heads 
     if (!q || !k || !v || !out || !cu_q || !cu_k || !q->data || !k->data || !v->data || !out->data)
         return BL_ERR_NULL;
     if (D != 128 || !valid_groups(H, Hkv) || batch < 1 || batch > 65535 || !(scale > 0.0f) ||
-        !(scale <= 3.0e38f) || (flags & ~BL_FLAG_PDL) || !valid_heads(*q, H) || !valid_heads(*k, Hkv) ||
+        !(scale <= 3.0e38f) || flags || !valid_heads(*q, H) || !valid_heads(*k, Hkv) ||
         !valid_heads(*v, Hkv) || !valid_heads(*out, H) || v->rows != k->rows || out->rows != q->rows ||
         !distinct_heads(*out, H))
         return BL_ERR_SHAPE;
@@ -764,7 +764,7 @@ int bitlinear_attention_prefill(const bitlinear_heads *q, const bitlinear_heads 
         return st;
     if (!ws || ws_bytes < attention_prefill_workspace_bytes(H, Hkv))
         return BL_ERR_WORKSPACE;
-    const PrefillArgs a{*q, *k, *v, *out, cu_q, cu_k, batch, H, Hkv, scale, ws, flags};
+    const PrefillArgs a{*q, *k, *v, *out, cu_q, cu_k, batch, H, Hkv, scale, ws};
     return launch_attention_prefill(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -789,7 +789,7 @@ int bitlinear_adapter_add(const void *y, int yt, int64_t ldy, const void *x, int
     if (!valid_dtype(yt))
         return BL_ERR_DTYPE;
     if (!valid_nk(N, K) || !valid_rank(T, r) || n < 1 || n > 65536 || ldy < N || ldo < N || ldx < K ||
-        (flags & ~BL_FLAG_PDL) || (out == y && ldo != ldy))
+        flags || (out == y && ldo != ldy))
         return BL_ERR_SHAPE;
     if (!aligned16(x) || !aligned16(down) || !aligned16(up) || ldx * 2 % 16 || !aligned16(ws) ||
         ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & (yt == BL_BF16 ? 1u : 3u)) ||
@@ -803,7 +803,7 @@ int bitlinear_adapter_add(const void *y, int yt, int64_t ldy, const void *x, int
         return st;
     if (!ws || ws_bytes < adapter_workspace_bytes(T, r))
         return BL_ERR_WORKSPACE;
-    const AdapterArgs a{y, yt, ldy, x, ldx, T, N, K, down, up, n, r, index, scale, out, ldo, ws, flags};
+    const AdapterArgs a{y, yt, ldy, x, ldx, T, N, K, down, up, n, r, index, scale, out, ldo, ws};
     return launch_adapter_add(a, static_cast<cudaStream_t>(stream));
 }
 

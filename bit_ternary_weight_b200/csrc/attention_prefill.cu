@@ -1154,15 +1154,34 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinSplit = 16;       // CTAs per cut tile
-constexpr int kJoinFew = 8;          // up to so many parts, a warp has a row to itself
+constexpr int kJoinSplit = 8;        // CTAs per cut tile, at most
+constexpr int kJoinFew = 8;          // up to so many parts, a warp takes four rows at once
 constexpr int kJoinLanes = 8;        // parts per lane: grids of up to 256 CTAs
 
-// CTA (c, y) takes every kJoinSplit-th row, or group of rows, of the tile
-// whose first part CTA c of the main kernel holds.  All of a row's (m, l) come
-// with one load per lane, then its O's with independent loads: few parts
-// (prompts), a warp per row; many (a long cache cut over the GPU), the CTA's
-// warps share a row's parts and add their sums in order.
+// A part's share of the sum: 2^(c (m_part - m)) of its l and O.  A part in which
+// the row sees no key has l = 0 and no O; NaN scores leave m at -inf and l NaN,
+// and the factor is NaN then.
+__device__ __forceinline__ float part_factor(float2 ml, float m, float c)
+{
+    return ml.y == 0.0f ? 0.0f : exp2f((ml.x - m) * c);
+}
+
+__device__ __forceinline__ void add_part(float4 &acc, float4 o, float f)
+{
+    if (f != 0.0f) {        // an O that was not written is not looked at
+        acc.x = fmaf(o.x, f, acc.x);
+        acc.y = fmaf(o.y, f, acc.y);
+        acc.z = fmaf(o.z, f, acc.z);
+        acc.w = fmaf(o.w, f, acc.w);
+    }
+}
+
+// CTA (c, y) takes every gridDim.y-th group of rows of the tile whose first
+// part CTA c of the main kernel holds.  The time is that of a few dependent
+// loads, so many rows go side by side: with few parts (prompts), four rows a
+// warp, whose (m, l) come with one load and whose O's with independent ones;
+// with many (a long cache cut over the GPU), the CTA's warps share a row's
+// parts and add their sums in order.
 template <bool PAIR>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const PrefillParams p)
 {
@@ -1177,76 +1196,100 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
     const int kvh = int(h0.y), q_row = int(h0.z), toks = int(h0.w), parts = int(h1.x) - c + 1;
     constexpr int64_t kSlotRows = PAIR ? 2 * kRows : kRows;
     const int rows = toks * p.G;
-    const bool few = parts <= kJoinFew;
-    const int step = few ? kJoinSplit * kJoinWarps : kJoinSplit;
-    for (int row = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; row < rows; row += step) {
-        const int tok = row / p.G, g = row - tok * p.G;     // token of the tile, head of the group
-        const int tile = PAIR ? tok / p.TM : 0;             // stream
-        const int64_t at = tile * kRows + (tok - tile * p.TM) * p.G + g;
-        // part i: the first is the slot of a tile's beginning, the others of a continuation
-        auto part_row = [&](int i) { return int64_t(i ? 2 * (c + i) : 2 * c + 1) * kSlotRows + at; };
-        float m = -INFINITY, pm[kJoinLanes], pl[kJoinLanes];
-#pragma unroll
-        for (int x = 0; x < kJoinLanes; ++x) {
-            const int i = 32 * x + lane;
-            const float2 ml = i < parts ? __ldcg(&p.part_ml[part_row(i)]) : make_float2(-INFINITY, 0.0f);
-            pm[x] = ml.x;
-            pl[x] = ml.y;
-            m = fmaxf(m, ml.x);
-        }
-        m = warp_max(m);
-        float l = 0.0f;
-#pragma unroll
-        for (int x = 0; x < kJoinLanes; ++x) {
-            // the part's factor; a part without a visible key has none (its O is not written).
-            // NaN scores leave m at -inf and l NaN: the factor is NaN then
-            const float f = pl[x] == 0.0f ? 0.0f : exp2f((pm[x] - m) * p.c);
-            l = fmaf(pl[x], f, l);
-            pm[x] = f;
-        }
-        l = warp_sum(l);
-        float4 acc = {};
-        auto add = [&](int i, float f) {
-            if (f == 0.0f)
-                return;
-            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + part_row(i) * kHD) + lane);
-            acc.x = fmaf(o.x, f, acc.x);
-            acc.y = fmaf(o.y, f, acc.y);
-            acc.z = fmaf(o.z, f, acc.z);
-            acc.w = fmaf(o.w, f, acc.w);
-        };
-        if (few) {
-#pragma unroll
-            for (int i = 0; i < kJoinFew; ++i)
-                if (i < parts)
-                    add(i, __shfl_sync(0xffffffffu, pm[0], i));
-        } else {
-            if (warp == 0) {
-#pragma unroll
-                for (int x = 0; x < kJoinLanes; ++x)
-                    fac_s[32 * x + lane] = pm[x];
-            }
-            __syncthreads();
-#pragma unroll 4
-            for (int i = warp; i < parts; i += kJoinWarps)
-                add(i, fac_s[i]);
-            acc_s[warp][lane] = acc;
-            __syncthreads();
-            if (warp == 0) {
-#pragma unroll
-                for (int w = 1; w < kJoinWarps; ++w) {
-                    const float4 o = acc_s[w][lane];
-                    acc = make_float4(acc.x + o.x, acc.y + o.y, acc.z + o.z, acc.w + o.w);
-                }
-            }
-            __syncthreads();
-            if (warp)
-                continue;
-        }
+    // row of part 0 in the workspace; part i: the first is the slot of a
+    // tile's beginning, the others of a continuation
+    auto slot_row = [&](int row) {
+        const int tok = row / p.G, tile = PAIR ? tok / p.TM : 0;
+        return tile * kRows + (tok - tile * p.TM) * p.G + (row - tok * p.G);
+    };
+    auto part_row = [&](int i, int at) { return int64_t(i ? 2 * (c + i) : 2 * c + 1) * kSlotRows + at; };
+    auto load_ml = [&](int i, int at) { return __ldcg(&p.part_ml[part_row(i, at)]); };
+    auto load_o = [&](int i, int at) {
+        return __ldcg(reinterpret_cast<const float4 *>(p.part_o + part_row(i, at) * kHD) + lane);
+    };
+    auto store = [&](int row, const float4 &acc, float l) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int tok = row / p.G, g = row - tok * p.G;
         __nv_bfloat16 *dst = p.out + int64_t(q_row + tok) * p.o_row + int64_t(kvh * p.G + g) * p.o_head;
         *reinterpret_cast<uint2 *>(dst + 4 * lane) =
             make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+    };
+    if (parts <= kJoinFew) {
+        for (int row0 = (blockIdx.y * kJoinWarps + warp) * 4; row0 < rows; row0 += gridDim.y * kJoinWarps * 4) {
+            // lane 8 r + i: row r, part i
+            const int mine = row0 + lane / 8, i = lane % 8;
+            const bool in = mine < rows && i < parts;
+            const float2 ml = in ? load_ml(i, slot_row(mine)) : make_float2(-INFINITY, 0.0f);
+            float m = ml.x;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float f = part_factor(ml, m, p.c);
+            float l = ml.y * f;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+            float4 acc[4] = {};
+            int at[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                at[r] = slot_row(min(row0 + r, rows - 1));
+#pragma unroll 2
+            for (int j = 0; j < parts; ++j) {
+                float4 o[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    o[r] = load_o(j, at[r]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    add_part(acc[r], o[r], __shfl_sync(0xffffffffu, f, 8 * r + j));
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float lr = __shfl_sync(0xffffffffu, l, 8 * r);
+                if (row0 + r < rows)
+                    store(row0 + r, acc[r], lr);
+            }
+        }
+        return;
+    }
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        const int at = slot_row(row);
+        float2 ml[kJoinLanes];
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kJoinLanes; ++x) {
+            const int i = 32 * x + lane;
+            ml[x] = i < parts ? load_ml(i, at) : make_float2(-INFINITY, 0.0f);
+            m = fmaxf(m, ml[x].x);
+        }
+        m = warp_max(m);
+#pragma unroll
+        for (int x = 0; x < kJoinLanes; ++x) {
+            const float f = part_factor(ml[x], m, p.c);
+            l = fmaf(ml[x].y, f, l);
+            if (warp == 0)
+                fac_s[32 * x + lane] = f;
+        }
+        l = warp_sum(l);
+        __syncthreads();
+        float4 acc = {};
+#pragma unroll 4
+        for (int i = warp; i < parts; i += kJoinWarps) {
+            const float f = fac_s[i];
+            add_part(acc, f != 0.0f ? load_o(i, at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f), f);
+        }
+        acc_s[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int w = 1; w < kJoinWarps; ++w) {
+                const float4 o = acc_s[w][lane];
+                acc = make_float4(acc.x + o.x, acc.y + o.y, acc.z + o.z, acc.w + o.w);
+            }
+            store(row, acc, l);
+        }
+        __syncthreads();
     }
 }
 
@@ -1304,7 +1347,7 @@ WsLayout ws_layout(int grid)
 
 template <bool PAIR>
 int launch_mode(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const PrefillParams &p, int grid,
-                unsigned flags, cudaStream_t s)
+                int64_t q_rows, cudaStream_t s)
 {
     int per_sm = 0;
     int st = occupancy(reinterpret_cast<const void *>(prefill_kernel<PAIR>), kThreads, smem_bytes<PAIR>(), &per_sm);
@@ -1321,13 +1364,14 @@ int launch_mode(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap 
     cfg.dynamicSmemBytes = smem_bytes<PAIR>();
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = flags & BL_FLAG_PDL ? 1 : 0;
+    cfg.numAttrs = 1;       // each kernel waits itself for what came before it
     if ((st = cuda_status(cudaLaunchKernelEx(&cfg, prefill_kernel<PAIR>, qm, km, vm, p))))
         return st;
-    cfg.gridDim = dim3(unsigned(grid), kJoinSplit);
+    // rows of a tile that there can be, eight warps a CTA
+    const int64_t rows = std::min<int64_t>(q_rows, (PAIR ? 2 : 1) * p.TM) * p.G;
+    cfg.gridDim = dim3(unsigned(grid), unsigned(std::clamp<int64_t>(rows, 1, kJoinSplit)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;       // it waits for the main kernel's results itself
     return cuda_status(cudaLaunchKernelEx(&cfg, prefill_join_kernel<PAIR>, p));
 }
 
@@ -1372,8 +1416,8 @@ int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s)
         return st;
     // two tiles of rows per CTA once every CTA could have a pair of them
     const int64_t pairs = int64_t(a.Hkv) * (p.Tq / (2 * p.TM));
-    return pairs >= grid / 4 ? launch_mode<true>(qm, km, vm, p, grid, a.flags, s)
-                             : launch_mode<false>(qm, km, vm, p, grid, a.flags, s);
+    return pairs >= grid / 4 ? launch_mode<true>(qm, km, vm, p, grid, p.Tq, s)
+                             : launch_mode<false>(qm, km, vm, p, grid, p.Tq, s);
 }
 
 }  // namespace bl

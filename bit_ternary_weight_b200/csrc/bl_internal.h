@@ -174,7 +174,6 @@ struct PrefillArgs {
     int batch, H, Hkv;
     float scale;
     void *ws;
-    unsigned flags;
 };
 size_t attention_prefill_workspace_bytes(int H, int Hkv);
 int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s);
@@ -192,7 +191,6 @@ struct AdapterArgs {
     void *out;
     int64_t ldo;
     void *ws;
-    unsigned flags;
 };
 size_t adapter_workspace_bytes(int64_t T, int r);
 int launch_adapter_add(const AdapterArgs &a, cudaStream_t s);

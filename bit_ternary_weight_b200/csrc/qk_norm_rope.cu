@@ -262,12 +262,11 @@ int launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t s)
     cfg.blockDim = dim3(kRopeThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    if (a.flags & BL_FLAG_PDL) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
+    // the kernel reads and writes nothing before what came before it is complete
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     const bool halves = a.flags & BL_FLAG_ROPE_HALVES;
     auto kernel = a.xt == BL_BF16 ? (halves ? qk_norm_rope_kernel<BL_BF16, true> : qk_norm_rope_kernel<BL_BF16, false>)
                                   : (halves ? qk_norm_rope_kernel<BL_F32, true> : qk_norm_rope_kernel<BL_F32, false>);

@@ -654,6 +654,13 @@ typedef struct {
 #define BL_FLAG_ROPE_HALVES 8u
 
 /*
+ * The next three operators take the rows of any number of requests at once.
+ * Their launches are always chained to the kernel before them on the stream
+ * (programmatic dependent launch): they begin while it ends, and read and
+ * write nothing before it is complete.
+ */
+
+/*
  * Queries and keys of T tokens of any number of requests in one pass: RMS
  * norm of each head (optional), rotation by the token's position, and keys
  * and values written to their cache rows.  Source: "bit-floor" README,
@@ -681,7 +688,7 @@ typedef struct {
  * position outside the table or a slot outside k_out records BL_ERR_SHAPE in
  * the device status word, and nothing is written for that token (position) or
  * for its key and value (slot).
- * 1 <= T < 2^31, H, Hkv <= 1024, D == 128.  flags: BL_FLAG_PDL, BL_FLAG_ROPE_HALVES.
+ * 1 <= T < 2^31, H, Hkv <= 1024, D == 128.  flags: 0 or BL_FLAG_ROPE_HALVES.
  */
 int bitlinear_qk_norm_rope(const bitlinear_heads *q, const bitlinear_heads *k, const bitlinear_heads *v,
                            int xt, int H, int Hkv, int D, const int32_t *positions,
@@ -722,7 +729,7 @@ size_t bitlinear_attention_prefill_workspace_bytes(int H, int Hkv);
  *   ws, ws_bytes device workspace, 16-byte aligned, of at least
  *                bitlinear_attention_prefill_workspace_bytes; its contents on
  *                entry are ignored.  Not shared by calls that can run at the same time.
- * 1 <= batch <= 65535; q, k with 1 .. 2^31 - 1 rows; strides below 2^38.  flags: BL_FLAG_PDL.
+ * 1 <= batch <= 65535; q, k with 1 .. 2^31 - 1 rows; strides below 2^38.  flags: 0.
  */
 int bitlinear_attention_prefill(const bitlinear_heads *q, const bitlinear_heads *k,
                                 const bitlinear_heads *v, const int32_t *cu_q,
@@ -756,7 +763,7 @@ size_t bitlinear_adapter_workspace_bytes(int64_t T, int r);
  * values (two, 16 bits of mantissa, for bf16 outputs, three for fp32 outputs).
  * Sums have a fixed order: the same call gives the same bits.
  * r a multiple of 8, 8 <= r <= 128; K % 64 == 0; x, down and up 16-byte
- * aligned, ldx such that rows are.  1 <= T < 2^31, 1 <= n <= 65536.  flags: BL_FLAG_PDL.
+ * aligned, ldx such that rows are.  1 <= T < 2^31, 1 <= n <= 65536.  flags: 0.
  */
 int bitlinear_adapter_add(const void *y, int yt, int64_t ldy, const void *x, int64_t ldx,
                           int64_t T, int64_t N, int64_t K, const void *down, const void *up,

@@ -159,7 +159,7 @@ def test_rope_argument_errors_before_any_cuda_call(bl):
                                     None) == bl.BL_ERR_NULL
     assert call(xt=5) == bl.BL_ERR_DTYPE
     assert call(qg=A, gt=7) == bl.BL_ERR_DTYPE
-    for kw in (dict(D=64), dict(H=0), dict(rows=0), dict(flags=2), dict(flags=64), dict(qg=A, eps=-1.0),
+    for kw in (dict(D=64), dict(H=0), dict(rows=0), dict(flags=1), dict(flags=64), dict(qg=A, eps=-1.0),
                dict(qg=A, eps=float("nan")), dict(q=_h(bl, rows=0)), dict(k=_h(bl, rows=7)), dict(q=_h(bl, row=64)),
                dict(k=_h(bl, head=0)), dict(ko=_h(bl, rows=7), vo=_h(bl, rows=7)), dict(vo=_h(bl, rows=9)),
                dict(qo=_h(bl, row=128)),                           # rows of an output on top of one another
