@@ -10,13 +10,21 @@
 // of attention.cu, so a prompt's cache rows equal the rows that its tokens
 // would get one at a time.
 //
-// Memory-bound: every element is read once and written once.  Eight lanes
-// take a head, each with dimensions 8c .. 8c + 7 and 64 + 8c .. 64 + 8c + 7, so
-// that every load and store of bf16 is 16 bytes a lane and 128 contiguous
-// bytes a head, and both kinds of pairs ((2i, 2i + 1) and (i, i + 64)) are
-// inside one lane; the mean square is a sum over three shuffles.  A warp takes
-// four heads at a time of one token, whose angles stay in registers, and asks
-// for several steps' heads before it knows the token's position.
+// Memory-bound: every element is read once and written once, so the design is
+// about bytes in flight.  A warp takes the heads of a token (or a part of
+// them), which one bulk copy per head, each issued by a lane, brings to a slot
+// of the warp's in shared memory, two slots a warp, so that one token arrives
+// while the other is worked on.  An 8192-token prompt of 20 + 5 + 5 heads
+// (126 MB): 32 us, 3.9 TB/s; with loads to registers, three steps of four heads
+// ahead, 39 us.  What bounds it is the arithmetic's latency at 12 warps an SM:
+// without any store it still takes 30 us.  (8 warps of three slots: 36 us.)
+// Eight lanes take a head from the slot, each
+// with dimensions 8c .. 8c + 7 and 64 + 8c .. 64 + 8c + 7, so that every access
+// is 16 bytes a lane and both kinds of pairs ((2i, 2i + 1) and (i, i + 64)) are
+// inside one lane; the mean square is a sum over three shuffles.  Two pairs go
+// through each arithmetic instruction (packed fp32), and what multiplies a
+// value is made once for a token's queries and once for its keys: with a
+// gain, x r g c is r (x (g c)).
 #include <algorithm>
 
 #include "bl_common.cuh"
@@ -25,8 +33,10 @@ namespace bl {
 namespace {
 
 constexpr int kHD = 128;
-constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = 12;
 constexpr int kHeadLanes = 8;
+constexpr int kRopeSlots = 2;             // items on their way per warp
+constexpr int kSlotBytes = 8192;          // 32 heads of bf16, 16 of fp32
 
 struct RopeParams {
     const void *q, *k, *v;
@@ -34,7 +44,9 @@ struct RopeParams {
     __nv_bfloat16 *qo, *ko, *vo;
     int64_t qo_row, qo_head, ko_row, ko_head, vo_row, vo_head;
     int T, H, Hkv, heads;          // heads: H + Hkv (+ Hkv with values)
-    int parts, steps;              // warps per token, steps of four heads each takes
+    int parts, part;               // parts of a token's heads, heads of each
+    int64_t items;                 // T * parts
+    bool runs;                     // the heads of a token's queries (keys, values) are contiguous
     const int32_t *positions;
     const float2 *table;
     int64_t table_rows;
@@ -55,156 +67,314 @@ __device__ __forceinline__ void gain8(const void *g, int gt, int at, float f[8])
         load8<BL_F32>(g, at, f);
 }
 
-// Eight elements as loaded: one 16-byte vector of bf16, two of fp32.
-template <int XT>
-struct Raw8 {
-    uint4 v[XT == BL_BF16 ? 1 : 2];
-    __device__ __forceinline__ void load(const void *base, int64_t at)
-    {
-        if constexpr (XT == BL_BF16) {
-            v[0] = ld_dep_v4(static_cast<const __nv_bfloat16 *>(base) + at);
-        } else {
-            v[0] = ld_dep_v4(static_cast<const float *>(base) + at);
-            v[1] = ld_dep_v4(static_cast<const float *>(base) + at + 4);
-        }
-    }
-    __device__ __forceinline__ void floats(float f[8]) const
-    {
-        if constexpr (XT == BL_BF16) {
-            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
-            const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = __uint_as_float(w[i]);
-        }
-    }
-};
-
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-__device__ __forceinline__ uint4 pack8(const float f[8])
-{
-    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-}
-
-__device__ __forceinline__ void rotate(float &a, float &b, float2 cs)
-{
-    const float r0 = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-    const float r1 = __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x));
-    a = r0;
-    b = r1;
-}
-
-template <int XT, bool HALVES>
-__global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_kernel(const RopeParams p)
-{
-    constexpr int kAhead = XT == BL_BF16 ? 3 : 2;        // steps whose heads are in flight
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t item = (int64_t(blockIdx.x) * kRopeThreads + threadIdx.x) / 32;
-    const int64_t t = item / p.parts;
-    if (t >= p.T)
-        return;
-    const int lane = threadIdx.x & 31, c = lane % kHeadLanes;
-    const int first = int(item - t * p.parts) * p.steps * 4 + lane / kHeadLanes;     // this lane's first head
-    const int last = min(p.heads, (int(item - t * p.parts) + 1) * p.steps * 4);
-    Raw8<XT> lo[kAhead], hi[kAhead];
-    auto load = [&](int h, Raw8<XT> &a, Raw8<XT> &b) {
-        if (h >= last)
-            return;
-        const void *src = h < p.H ? p.q : h < p.H + p.Hkv ? p.k : p.v;
-        const int64_t at = h < p.H            ? t * p.q_row + h * p.q_head
-                           : h < p.H + p.Hkv ? t * p.k_row + (h - p.H) * p.k_head
-                                              : t * p.v_row + (h - p.H - p.Hkv) * p.v_head;
-        a.load(src, at + 8 * c);
-        b.load(src, at + 64 + 8 * c);
-    };
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-        load(first + 4 * u, lo[u], hi[u]);
-    const int64_t pos = int32_t(ld_dep_u32(p.positions + t));
-    int64_t row = p.slots ? int32_t(ld_dep_u32(p.slots + t)) : t;
-    const bool bad_pos = pos < 0 || pos >= p.table_rows, bad_row = p.slots && row >= p.out_rows;
-    if (bad_pos || bad_row) {
-        if (lane == 0)
-            atomicExch(p.status, BL_ERR_SHAPE);
-        if (bad_pos)
-            return;
-        row = -1;
+// Two fp32 values in one register pair, and what is done to both at once.
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+    __device__ __forceinline__ void get(float &lo, float &hi) const
+    {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
     }
-    // (cos, sin) of this lane's pairs: 8c .. 8c + 7, or 4c .. 4c + 3 and 32 + 4c .. 32 + 4c + 3
-    const float2 *tab = p.table + pos * (kHD / 2);
-    float2 cs[8];
+};
+__device__ __forceinline__ F2 mul(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b)
+{
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+
+// A lane's sixteen elements of a head: 8c .. 8c + 7 and 64 + 8c .. 64 + 8c + 7.
+template <int XT>
+struct Raw {
+    static constexpr int kVecs = XT == BL_BF16 ? 1 : 2;
+    uint4 v[2][kVecs];
+    __device__ __forceinline__ void load(const unsigned char *head, int c)
+    {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        cs[i] = __ldg(tab + (HALVES ? 8 * c + i : i < 4 ? 4 * c + i : 32 + 4 * c + i - 4));
-    // gains of the kind of head (0: query, 1: key) that was taken last
-    float ga[8], gb[8];
-    int kind = -1;
-    for (int h0 = first; h0 - lane / kHeadLanes < last; h0 += 4 * kAhead) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int h = h0 + 4 * u;
-            if (h - lane / kHeadLanes >= last)
-                break;
-            float a[8], b[8];
-            lo[u].floats(a);
-            hi[u].floats(b);
-            const bool is_q = h < p.H, is_k = !is_q && h < p.H + p.Hkv;
-            const void *gain = is_q ? p.q_gain : is_k ? p.k_gain : nullptr;
-            float s = 0.0f;
+            for (int i = 0; i < kVecs; ++i)
+                v[h][i] = *reinterpret_cast<const uint4 *>(head + (h * 64 + 8 * c) * (XT == BL_BF16 ? 2 : 4) + 16 * i);
+    }
+    // Elements e and e + 1 (e even) of half h.
+    __device__ __forceinline__ void two(int h, int e, float &x, float &y) const
+    {
+        const uint4 &q = v[h][XT == BL_BF16 ? 0 : e / 4];
+        if constexpr (XT == BL_BF16) {
+            const uint32_t w = e == 0 ? q.x : e == 2 ? q.y : e == 4 ? q.z : q.w;
+            x = __uint_as_float(w << 16);
+            y = __uint_as_float(w & 0xffff0000u);
+        } else {
+            x = __uint_as_float(e % 4 ? q.z : q.x);
+            y = __uint_as_float(e % 4 ? q.w : q.y);
+        }
+    }
+    // Pairs (a, b) number 2j and 2j + 1 of the lane's eight.
+    template <bool HALVES>
+    __device__ __forceinline__ void pairs(int j, F2 &a, F2 &b) const
+    {
+        float x0, x1, y0, y1;
+        if (HALVES) {
+            two(0, 2 * j, x0, x1);
+            two(1, 2 * j, y0, y1);
+            a = F2(x0, x1);
+            b = F2(y0, y1);
+        } else {
+            two(j / 2, 4 * (j % 2), x0, x1);
+            two(j / 2, 4 * (j % 2) + 2, y0, y1);
+            a = F2(x0, y0);
+            b = F2(x1, y1);
+        }
+    }
+};
+
+// Norm (NORM) and rotation of every fourth head from `src`, eight lanes a head;
+// `left` heads remain from this group's first on.
+//   (a, b) -> (a c1 + b s1, a s2 + b c2) with c1 = g_a c, s1 = -g_b s, s2 = g_a s,
+//   c2 = g_b c, pairs two by two (g = 1 without a norm)
+template <int XT, bool HALVES, bool NORM>
+__device__ __forceinline__ void rotate_heads(const unsigned char *src, __nv_bfloat16 *dst, int64_t ohead, int left,
+                                             int group, int c, const float2 (&cs)[8], const void *gain, int gt, float eps)
+{
+    constexpr int kHeadBytes = kHD * (XT == BL_BF16 ? 2 : 4);
+    F2 c1[4], s1[4], s2[4], c2[4];
+    float gl[8], gh[8];
+    if (NORM) {
+        gain8(gain, gt, 8 * c, gl);
+        gain8(gain, gt, 64 + 8 * c, gh);
+    }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
+    for (int j = 0; j < 4; ++j) {
+        const float2 x = cs[2 * j], y = cs[2 * j + 1];
+        c1[j] = c2[j] = F2(x.x, y.x);
+        s2[j] = F2(x.y, y.y);
+        s1[j] = F2(-x.y, -y.y);
+        if (NORM) {
+            const float *g = j < 2 ? gl : gh;
+            const F2 ga = HALVES ? F2(gl[2 * j], gl[2 * j + 1]) : F2(g[4 * (j % 2)], g[4 * (j % 2) + 2]);
+            const F2 gb = HALVES ? F2(gh[2 * j], gh[2 * j + 1]) : F2(g[4 * (j % 2) + 1], g[4 * (j % 2) + 3]);
+            c1[j] = mul(c1[j], ga);
+            s2[j] = mul(s2[j], ga);
+            s1[j] = mul(s1[j], gb);
+            c2[j] = mul(c2[j], gb);
+        }
+    }
+    const int64_t ostep = 4 * ohead;
+#pragma unroll 2
+    for (int more = left + group; more > 0; more -= 4, src += 4 * kHeadBytes, dst += ostep) {
+        // a group behind the last head computes on what lies there and stores nothing
+        Raw<XT> x;
+        x.load(src, c);
+        F2 a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x.template pairs<HALVES>(j, a[j], b[j]);
+        F2 r2;
+        if (NORM) {
+            F2 sum = mul(a[0], a[0]), sum1 = mul(b[0], b[0]);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) {
+                sum = fma(a[j], a[j], sum);
+                sum1 = fma(b[j], b[j], sum1);
+            }
+            float s0, s;
+            add(sum, sum1).get(s0, s);
+            s += s0;
 #pragma unroll
             for (int o = kHeadLanes / 2; o > 0; o >>= 1)
                 s += __shfl_xor_sync(0xffffffffu, s, o);
-            load(h + 4 * kAhead, lo[u], hi[u]);
-            if (h >= last || (!is_q && row < 0))
-                continue;
-            if (gain) {
-                if (kind != int(is_k)) {
-                    kind = is_k;
-                    gain8(gain, p.gt, 8 * c, ga);
-                    gain8(gain, p.gt, 64 + 8 * c, gb);
-                }
-                // fp32 to 2^-22; the result rounds at 2^-8
-                const float r = rsqrtf(fmaf(s, 1.0f / kHD, p.eps));
+            // fp32 to 2^-22; the result rounds at 2^-8
+            s = rsqrtf(fmaf(s, 1.0f / kHD, eps));
+            r2 = F2(s, s);
+        }
+        uint32_t w[2][4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a[i] = a[i] * r * ga[i];
-                    b[i] = b[i] * r * gb[i];
-                }
+        for (int j = 0; j < 4; ++j) {
+            F2 o0, o1;
+            if (NORM) {
+                o0 = mul(fma(a[j], c1[j], mul(b[j], s1[j])), r2);
+                o1 = mul(fma(a[j], s2[j], mul(b[j], c2[j])), r2);
+            } else {
+                o0 = add(mul(a[j], c1[j]), mul(b[j], s1[j]));
+                o1 = add(mul(a[j], s2[j]), mul(b[j], c2[j]));
             }
-            if (is_q || is_k) {
-                if (HALVES) {
+            float a0, a1, b0, b1;
+            o0.get(a0, a1);
+            o1.get(b0, b1);
+            if (HALVES) {
+                w[0][j] = pack2(a0, a1);
+                w[1][j] = pack2(b0, b1);
+            } else {
+                w[j / 2][2 * (j % 2)] = pack2(a0, b0);
+                w[j / 2][2 * (j % 2) + 1] = pack2(a1, b1);
+            }
+        }
+        if (more > group) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+            *reinterpret_cast<uint4 *>(dst + 64) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+        }
+    }
+}
+
+struct RopeSmem {
+    alignas(128) unsigned char slot[kRopeWarps][kRopeSlots][kSlotBytes];
+    unsigned char behind[3 * 4 * kHD];   // what the groups behind the last head of the last slot read
+    uint64_t full[kRopeWarps][kRopeSlots];
+    int abort_flag;
+};
+
+template <int XT, bool HALVES>
+__global__ void __launch_bounds__(kRopeWarps * 32, 1) qk_norm_rope_kernel(const RopeParams p)
+{
+    extern __shared__ __align__(128) unsigned char rope_raw[];
+    RopeSmem &sm = *reinterpret_cast<RopeSmem *>(rope_raw);
+    constexpr uint32_t kHeadBytes = kHD * (XT == BL_BF16 ? 2 : 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kHeadLanes;
+    if (lane == 0) {
+        for (int i = 0; i < kRopeSlots; ++i)
+            mbar_init(smem_u32(&sm.full[warp][i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (warp == 0)
+            sm.abort_flag = 0;
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t stride = int64_t(gridDim.x) * kRopeWarps;
+    const int64_t item0 = int64_t(blockIdx.x) * kRopeWarps + warp;
+    auto token = [&](int64_t item) { return p.parts == 1 ? item : item / p.parts; };
+    // the heads of an item to slot i
+    auto fetch = [&](int64_t item, int i) {
+        if (item >= p.items)
+            return;
+        const int64_t t = token(item);
+        const int h0 = int(item - t * p.parts) * p.part, n = min(p.part, p.heads - h0);
+        const uint32_t bar = smem_u32(&sm.full[warp][i]);
+        if (lane == 0)
+            mbar_arrive_tx(bar, n * kHeadBytes);
+        __syncwarp();
+        // heads that lie one behind the other in one copy: lane 0, 1, 2 for
+        // queries, keys, values; else a head per lane
+        const int h = p.runs ? max(h0, lane == 0 ? 0 : lane == 1 ? p.H : p.H + p.Hkv) : h0 + lane;
+        const int stop = min(h0 + n, !p.runs ? h + 1 : lane == 0 ? p.H : lane == 1 ? p.H + p.Hkv : p.heads);
+        if (h < stop && (!p.runs || lane < 3)) {
+            const void *src = h < p.H ? p.q : h < p.H + p.Hkv ? p.k : p.v;
+            const int64_t at = h < p.H            ? t * p.q_row + h * p.q_head
+                               : h < p.H + p.Hkv ? t * p.k_row + (h - p.H) * p.k_head
+                                                  : t * p.v_row + (h - p.H - p.Hkv) * p.v_head;
+            bulk_load(smem_u32(&sm.slot[warp][i][(h - h0) * kHeadBytes]),
+                      static_cast<const char *>(src) + at * (XT == BL_BF16 ? 2 : 4), (stop - h) * kHeadBytes, bar);
+        }
+    };
+    auto position = [&](int64_t item) { return item < p.items ? int(ld_dep_u32(p.positions + token(item))) : 0; };
+    auto slot_row = [&](int64_t item) {
+        return item < p.items && p.slots ? int(ld_dep_u32(p.slots + token(item))) : 0;
+    };
+    for (int i = 0; i < kRopeSlots; ++i)
+        fetch(item0 + i * stride, i);
+    int pos = position(item0), srow = slot_row(item0);
+    int pos1 = position(item0 + stride), srow1 = slot_row(item0 + stride);
+    uint32_t phase = 0;
+    int slot = 0;
+    for (int64_t item = item0; item < p.items; item += stride) {
+        const int pos2 = position(item + 2 * stride), srow2 = slot_row(item + 2 * stride);
+        const int64_t t = token(item);
+        const int h0 = int(item - t * p.parts) * p.part, end = min(h0 + p.part, p.heads);
+        int64_t row = p.slots ? srow : t;
+        const bool bad_pos = pos < 0 || pos >= p.table_rows, bad_row = p.slots && row >= p.out_rows;
+        if ((bad_pos || bad_row) && lane == 0)
+            atomicExch(p.status, BL_ERR_SHAPE);
+        if (bad_row)
+            row = -1;
+        // (cos, sin) of the lane's pairs, on their way while the heads arrive:
+        // pairs 8c .. 8c + 7, or 4c .. 4c + 3 and 32 + 4c .. 32 + 4c + 3
+        float2 cs[8];
+        const float2 *tab = p.table + int64_t(bad_pos ? 0 : pos) * (kHD / 2);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        rotate(a[i], b[i], cs[i]);
-                } else {
+        for (int j = 0; j < 8; ++j)
+            cs[j] = __ldg(tab + (HALVES ? 8 * c : j < 4 ? 4 * c : 32 + 4 * c - 4) + j);
+        if (!mbar_wait_fast(smem_u32(&sm.full[warp][slot]), phase, &sm.abort_flag, p.status)) {
+            // given up: the copies on their way have landed before the CTA exits
+            volatile int no_abort = 0;
+            for (int i = 0; i < kRopeSlots && item + i * stride < p.items; ++i) {
+                mbar_wait(smem_u32(&sm.full[warp][slot]), phase, &no_abort, p.status, 100000000ull);
+                phase ^= slot == kRopeSlots - 1;
+                slot = slot == kRopeSlots - 1 ? 0 : slot + 1;
+            }
+            break;
+        }
+        const int group = lane / kHeadLanes;
+#pragma unroll 1
+        for (int kind = 0; kind < 3; ++kind) {
+            // this item's queries, keys or values: heads lo .. hi - 1
+            const int begin = kind == 0 ? 0 : kind == 1 ? p.H : p.H + p.Hkv;
+            const int lo = max(h0, begin), hi = min(end, kind == 0 ? p.H : kind == 1 ? p.H + p.Hkv : p.heads);
+            if (lo >= hi || bad_pos || (kind > 0 && row < 0))
+                continue;
+            const int64_t ohead = kind == 0 ? p.qo_head : kind == 1 ? p.ko_head : p.vo_head;
+            __nv_bfloat16 *dst = (kind == 0   ? p.qo + t * p.qo_row
+                                  : kind == 1 ? p.ko + row * p.ko_row
+                                              : p.vo + row * p.vo_row) + (lo - begin + group) * ohead + 8 * c;
+            const unsigned char *src = &sm.slot[warp][slot][(lo - h0 + group) * kHeadBytes];
+            int left = hi - lo - group;         // > 0: this group has a head
+            if (kind == 2) {
+                for (; left + group > 0; left -= 4, src += 4 * kHeadBytes, dst += 4 * ohead) {
+                    if (left <= 0)
+                        continue;
+                    Raw<XT> x;
+                    x.load(src, c);
+                    if constexpr (XT == BL_BF16) {
+                        *reinterpret_cast<uint4 *>(dst) = x.v[0][0];
+                        *reinterpret_cast<uint4 *>(dst + 64) = x.v[1][0];
+                    } else {
+                        uint32_t w[2][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        rotate(a[2 * i], a[2 * i + 1], cs[i]);
-                        rotate(b[2 * i], b[2 * i + 1], cs[4 + i]);
+                        for (int e = 0; e < 8; ++e) {
+                            float a, b;
+                            x.two(e / 4, 2 * (e % 4), a, b);
+                            w[e / 4][e % 4] = pack2(a, b);
+                        }
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+                        *reinterpret_cast<uint4 *>(dst + 64) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
                     }
                 }
+                continue;
             }
-            __nv_bfloat16 *dst = is_q   ? p.qo + t * p.qo_row + h * p.qo_head
-                                 : is_k ? p.ko + row * p.ko_row + (h - p.H) * p.ko_head
-                                        : p.vo + row * p.vo_row + (h - p.H - p.Hkv) * p.vo_head;
-            *reinterpret_cast<uint4 *>(dst + 8 * c) = pack8(a);
-            *reinterpret_cast<uint4 *>(dst + 64 + 8 * c) = pack8(b);
+            const void *gain = kind ? p.k_gain : p.q_gain;
+            if (gain)
+                rotate_heads<XT, HALVES, true>(src, dst, ohead, left, group, c, cs, gain, p.gt, p.eps);
+            else
+                rotate_heads<XT, HALVES, false>(src, dst, ohead, left, group, c, cs, nullptr, 0, 0.0f);
         }
+        __syncwarp();       // every lane has taken its part of the slot
+        fetch(item + kRopeSlots * stride, slot);
+        if (++slot == kRopeSlots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+        pos = pos1;
+        srow = srow1;
+        pos1 = pos2;
+        srow1 = srow2;
     }
 }
 
@@ -248,18 +418,21 @@ int launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t s)
     p.slots = a.slots;
     p.out_rows = a.k_out.rows;
     p.status = di->status;
-    // a token's heads go to one warp where the tokens fill the GPU (two
-    // CTAs' warps per SM and more), else to as many as there are steps
-    const int all = (p.heads + 3) / 4;
-    p.parts = int(std::clamp<int64_t>(int64_t(di->sm_count) * 16 / p.T, 1, all));
-    p.steps = (all + p.parts - 1) / p.parts;
-    p.parts = (all + p.steps - 1) / p.steps;
-    const int64_t blocks = (int64_t(p.T) * p.parts * 32 + kRopeThreads - 1) / kRopeThreads;
-    if (blocks > 0x7fffffff)
-        return BL_ERR_SHAPE;
+    // a token's heads go to as many warps as there are for it, four heads a
+    // warp or more, and as a slot needs them to
+    const int64_t warps = int64_t(di->sm_count) * kRopeWarps;
+    const int room = kSlotBytes / (kHD * (a.xt == BL_BF16 ? 2 : 4)), fours = (p.heads + 3) / 4;
+    const int64_t want = std::clamp<int64_t>(warps / p.T, 1, fours);
+    p.part = std::min(room, int((fours + want - 1) / want) * 4);
+    p.parts = (p.heads + p.part - 1) / p.part;
+    p.items = int64_t(p.T) * p.parts;
+    auto run = [](const bitlinear_heads &h, int heads) { return heads == 1 || h.head_stride == kHD; };
+    p.runs = run(a.q, a.H) && run(a.k, a.Hkv) && (!a.v.data || run(a.v, a.Hkv));
+    const int64_t blocks = std::min<int64_t>(di->sm_count, (p.items + kRopeWarps - 1) / kRopeWarps);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(blocks));
-    cfg.blockDim = dim3(kRopeThreads);
+    cfg.blockDim = dim3(kRopeWarps * 32);
+    cfg.dynamicSmemBytes = sizeof(RopeSmem);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     // the kernel reads and writes nothing before what came before it is complete
@@ -270,6 +443,12 @@ int launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t s)
     const bool halves = a.flags & BL_FLAG_ROPE_HALVES;
     auto kernel = a.xt == BL_BF16 ? (halves ? qk_norm_rope_kernel<BL_BF16, true> : qk_norm_rope_kernel<BL_BF16, false>)
                                   : (halves ? qk_norm_rope_kernel<BL_F32, true> : qk_norm_rope_kernel<BL_F32, false>);
+    int per_sm = 0;
+    const int st = occupancy(reinterpret_cast<const void *>(kernel), kRopeWarps * 32, sizeof(RopeSmem), &per_sm);
+    if (st)
+        return st;
+    if (per_sm < 1)
+        return BL_ERR_UNSUPPORTED;
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
