@@ -48,7 +48,6 @@ struct AdapterParams {
     float *u;                             // [splits][T][r]
     int splits;
     int down_ways;                        // CTAs that share the adapters of a tile
-    int vec;                              // y and out rows take 16-byte vectors
     int *status;
 };
 
@@ -102,43 +101,54 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int64_t t0 = int64_t(blockIdx.x) * kTile;
     const int way = blockIdx.y, split = blockIdx.z;
+    const int groups = int(p.K / 32);
+    const int k0 = int(int64_t(split) * groups / p.splits) + warp, k1 = int(int64_t(split + 1) * groups / p.splits);
+    constexpr int kDeep = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;      // groups in flight
+    const bool in0 = t0 + g < p.T, in1 = t0 + g + 8 < p.T;
+    const __nv_bfloat16 *x0 = p.x + (t0 + g) * p.ldx + 8 * c, *x1 = x0 + 8 * p.ldx;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    // all tokens' x, before their adapters are known: the rows of other
+    // adapters are dropped at the end
+    uint4 xa[kDeep], xb[kDeep];
+    auto load_x = [&](int k) {
+#pragma unroll
+        for (int s = 0; s < kDeep; ++s) {
+            const bool in = k + s * kDownWarps < k1;
+            const int64_t at = int64_t(k + s * kDownWarps) * 32;
+            xa[s] = in && in0 ? ld_dep_v4(x0 + at) : zero;
+            xb[s] = in && in1 ? ld_dep_v4(x1 + at) : zero;
+        }
+    };
+    load_x(k0);
+    const bool once = k0 + kDeep * kDownWarps >= k1;          // that was all of it
     const int id = tile_id(p, t0, lane, way == 0 && split == 0);
     unsigned firsts = first_of(id, lane);
-    const int groups = int(p.K / 32);
-    const int k0 = int(int64_t(split) * groups / p.splits), k1 = int(int64_t(split + 1) * groups / p.splits);
     for (int ord = 0; firsts; ++ord, firsts &= firsts - 1) {
         if (ord % p.down_ways != way)
             continue;
         const int a = __shfl_sync(0xffffffffu, id, __ffs(firsts) - 1);
         const unsigned rows = __ballot_sync(0xffffffffu, id == a);
-        const bool r0 = rows >> g & 1, r1 = rows >> (g + 8) & 1;
-        const __nv_bfloat16 *x0 = p.x + (t0 + g) * p.ldx + 8 * c, *x1 = x0 + 8 * p.ldx;
         const __nv_bfloat16 *w = p.down + (int64_t(a) * p.r + g) * p.K + 8 * c;
         float acc[NT][4] = {};
-        auto step = [&](const uint4 &xa, const uint4 &xb, const uint4 (&b)[NT]) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                mma_bf16(acc[j], xa.x, xb.x, xa.y, xb.y, b[j].x, b[j].y);
-                mma_bf16(acc[j], xa.z, xb.z, xa.w, xb.w, b[j].z, b[j].w);
-            }
-        };
-        constexpr int kDeep = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;      // groups in flight
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int k = k0 + warp; k < k1; k += kDeep * kDownWarps) {
-            uint4 xa[kDeep], xb[kDeep], b[kDeep][NT];
+        for (int k = k0; k < k1; k += kDeep * kDownWarps) {
+            uint4 b[kDeep][NT];
+            if (!once)
+                load_x(k);
 #pragma unroll
             for (int s = 0; s < kDeep; ++s) {
                 const int64_t at = int64_t(k + s * kDownWarps) * 32;
-                const bool in = k + s * kDownWarps < k1;
-                xa[s] = in && r0 ? ld_dep_v4(x0 + at) : zero;
-                xb[s] = in && r1 ? ld_dep_v4(x1 + at) : zero;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    b[s][j] = in && j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
+                    b[s][j] = k + s * kDownWarps < k1 && j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
             }
 #pragma unroll
-            for (int s = 0; s < kDeep; ++s)
-                step(xa[s], xb[s], b[s]);
+            for (int s = 0; s < kDeep; ++s) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mma_bf16(acc[j], xa[s].x, xb[s].x, xa[s].y, xb[s].y, b[s][j].x, b[s][j].y);
+                    mma_bf16(acc[j], xa[s].z, xb[s].z, xa[s].w, xb[s].w, b[s][j].z, b[s][j].w);
+                }
+            }
         }
         // sums of warps w and w + 4, then of the four pairs
         const int pair = warp & (kDownWarps / 2 - 1);
@@ -170,34 +180,29 @@ __global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const Ada
     }
 }
 
-// Eight consecutive columns n .. n + 7 of row t of y, as loaded: 16-byte
-// vectors, or one element after the other where rows are not aligned or end.
-template <bool F32>
+// Eight consecutive elements of a row, as loaded: 16-byte vectors (VEC), or one
+// element after the other where rows are not aligned or end inside the eight
+// (`left` of them are there).
+template <bool F32, bool VEC>
 struct Cols {
     uint4 v[F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const AdapterParams &p, int64_t t, int64_t n)
+    __device__ __forceinline__ void load(const char *src, int64_t left)
     {
-        const int64_t at = t * p.ldy + n;
-        if (p.vec && n + 8 <= p.N) {
-            const char *src = static_cast<const char *>(p.y) + at * (F32 ? 4 : 2);
+        if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < (F32 ? 2 : 1); ++i)
                 v[i] = ld_dep_v4(src + 16 * i);
-            return;
-        }
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = 0;
-            if (n + i < p.N)
-                w[i] = F32 ? ld_dep_u32(static_cast<const float *>(p.y) + at + i)
-                           : ld_dep_u16(static_cast<const __nv_bfloat16 *>(p.y) + at + i);
-        }
-        if constexpr (F32) {
-            v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            v[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
-            v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = i >= left ? 0u : F32 ? ld_dep_u32(src + 4 * i) : ld_dep_u16(src + 2 * i);
+            if constexpr (F32) {
+                v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+                v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+            }
         }
     }
     __device__ __forceinline__ void floats(float (&f)[8]) const
@@ -218,31 +223,22 @@ struct Cols {
             }
         }
     }
-};
-
-template <bool F32>
-__device__ __forceinline__ void store_cols(const AdapterParams &p, int64_t t, int64_t n, const float (&f)[8])
-{
-    const int64_t at = t * p.ldo + n;
-    if (p.vec && n + 8 <= p.N) {
-        if (F32) {
-            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
-            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+    static __device__ __forceinline__ void store(char *dst, const float (&f)[8], int64_t left)
+    {
+        if constexpr (VEC && F32) {
+            reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
+            reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else if constexpr (VEC) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                         pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
         } else {
-            uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 8; ++i)
+                if (i < left)
+                    store_y(dst, F32 ? BL_F32 : BL_BF16, i, f[i]);
         }
-        return;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (n + i < p.N)
-            store_y(p.out, F32 ? BL_F32 : BL_BF16, at + i, f[i]);
-}
+};
 
 // The values (a, b) as sums of TERMS bf16 values, largest first.
 template <int TERMS>
@@ -265,7 +261,7 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[TERMS
 // share one adapter (most tiles of a prompt) keeps its operand from tile to
 // tile and starts the accumulators at y (bf16 outputs; an fp32 output adds y at
 // the end, since a tensor core's sums lose up to 2^-23 of y each).
-template <int KB, bool F32, int WAYS>
+template <int KB, bool F32, int WAYS, bool VEC>
 __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const AdapterParams p)
 {
     constexpr int kTiles = WAYS == 1 ? (F32 ? 2 : 4) : 1;
@@ -278,7 +274,10 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
     const int way = WAYS == 1 ? 0 : warp;
     const int64_t n0 = (int64_t(blockIdx.x) * (kUpWarps / WAYS) + (WAYS == 1 ? warp : 0)) * kUpCols;
     const int64_t nc = n0 + 8 * c;                            // this lane's output columns
+    const int64_t left = p.N - nc;                            // columns from there to the row's end
     const bool cols = n0 < p.N;
+    constexpr int kElem = F32 ? 4 : 2;
+    using Eight = Cols<F32, VEC>;
     bool waited = false;
     constexpr int kKept = KB <= 2 ? KB : 1;                   // k blocks of an adapter's operand in registers
     uint2 b[kKept][4];
@@ -306,14 +305,14 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
         const int64_t t0 = run * kTokens;
         const int tokens = int(min(int64_t(kTokens), p.T - t0));
         __syncthreads();                                      // the last run's u has been used
-        Cols<F32> y[kTiles][2];
-        if (cols) {
+        Eight y[kTiles][2];
+        {
+            const char *src = static_cast<const char *>(p.y) + ((t0 + g) * p.ldy + nc) * kElem;
+            const int64_t step = 8 * p.ldy * kElem;
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (16 * i + 8 * h + g < tokens)
-                        y[i][h].load(p, t0 + 16 * i + 8 * h + g, nc);
+            for (int i = 0; i < 2 * kTiles; ++i, src += step)
+                if (8 * i + g < tokens && left > 0)
+                    y[i / 2][i % 2].load(src, left);
         }
         if (threadIdx.x < kTokens) {
             const int id = int(threadIdx.x) < tokens ? int(ld_dep_u32(p.index + t0 + threadIdx.x)) : -1;
@@ -348,11 +347,12 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
         __syncthreads();
         if (!cols)
             continue;
+        char *dst = static_cast<char *>(p.out) + ((t0 + g) * p.ldo + nc) * kElem;
+        const int64_t ostep = 8 * p.ldo * kElem;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
+        for (int i = 0; i < kTiles; ++i, dst += 2 * ostep) {
             if (16 * i >= tokens)
                 break;
-            const int64_t ta = t0 + 16 * i + g, tb = ta + 8;
             // acc += up u of adapter a for all 16 tokens (rows of other
             // adapters are dropped by the caller)
             auto product = [&](int a, float (&acc)[4][4]) {
@@ -395,8 +395,8 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
                         f[2 * x] = acc[x][2 * h];
                         f[2 * x + 1] = acc[x][2 * h + 1];
                     }
-                    if (g + 8 * h < valid)
-                        store_cols<F32>(p, h ? tb : ta, nc, f);
+                    if (g + 8 * h < valid && left > 0)
+                        Eight::store(dst + h * ostep, f, left);
                 }
                 continue;
             }
@@ -405,10 +405,10 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
             if (way == 0) {                                   // tokens without an adapter
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (none >> (g + 8 * h) & 1) {
+                    if ((none >> (g + 8 * h) & 1) && left > 0) {
                         float f[8];
                         y[i][h].floats(f);
-                        store_cols<F32>(p, h ? tb : ta, nc, f);
+                        Eight::store(dst + h * ostep, f, left);
                     }
                 }
             }
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
                 product(a, acc);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (rows >> (g + 8 * h) & 1) {
+                    if ((rows >> (g + 8 * h) & 1) && left > 0) {
                         float f[8];
                         y[i][h].floats(f);
 #pragma unroll
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
                             f[2 * x] += acc[x][2 * h];
                             f[2 * x + 1] += acc[x][2 * h + 1];
                         }
-                        store_cols<F32>(p, h ? tb : ta, nc, f);
+                        Eight::store(dst + h * ostep, f, left);
                     }
                 }
             }
@@ -460,13 +460,20 @@ cudaError_t launch(void (*kernel)(AdapterParams), dim3 grid, int threads, cudaSt
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <bool F32, int WAYS>
+template <bool F32, int WAYS, bool VEC>
 auto up_kernel(int r) -> void (*)(AdapterParams)
 {
-    return r <= 16   ? adapter_up_kernel<1, F32, WAYS>
-           : r <= 32 ? adapter_up_kernel<2, F32, WAYS>
-           : r <= 64 ? adapter_up_kernel<4, F32, WAYS>
-                     : adapter_up_kernel<8, F32, WAYS>;
+    return r <= 16   ? adapter_up_kernel<1, F32, WAYS, VEC>
+           : r <= 32 ? adapter_up_kernel<2, F32, WAYS, VEC>
+           : r <= 64 ? adapter_up_kernel<4, F32, WAYS, VEC>
+                     : adapter_up_kernel<8, F32, WAYS, VEC>;
+}
+
+template <bool F32>
+auto up_kernel(int r, bool few, bool vec) -> void (*)(AdapterParams)
+{
+    return few ? (vec ? up_kernel<F32, 8, true>(r) : up_kernel<F32, 8, false>(r))
+               : (vec ? up_kernel<F32, 1, true>(r) : up_kernel<F32, 1, false>(r));
 }
 
 }  // namespace
@@ -484,7 +491,7 @@ int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
         return BL_ERR_CUDA;
     const int64_t tiles = (a.T + kTile - 1) / kTile;
     const int esz = a.yt == BL_BF16 ? 2 : 4;
-    auto vec = [&](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * esz % 16 == 0; };
+    auto aligned = [&](const void *q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * esz % 16 == 0; };
     AdapterParams p{};
     p.y = a.y;
     p.ldy = a.ldy;
@@ -503,7 +510,6 @@ int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
     p.ldo = a.ldo;
     p.u = static_cast<float *>(a.ws);
     p.splits = int(std::clamp<int64_t>(a.K / 32 / kDownWarps, 1, max_splits(a.T, di->sm_count)));
-    p.vec = vec(a.y, a.ldy) && vec(a.out, a.ldo);
     p.status = di->status;
     // a tile's adapters go to CTAs of their own while tiles alone do not fill the GPU
     p.down_ways = int(std::clamp<int64_t>(di->sm_count / tiles, 1, std::min<int64_t>({kTile, a.n, a.T})));
@@ -520,8 +526,9 @@ int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
     const bool few = tiles * ((a.N + 8 * kUpCols - 1) / (8 * kUpCols)) < 2 * di->sm_count;
     const int cols = few ? kUpCols : kUpWarps * kUpCols, tokens = kTile * (few ? 1 : a.yt == BL_F32 ? 2 : 4);
     const int64_t gx = (a.N + cols - 1) / cols, gy = (a.T + tokens - 1) / tokens;
-    auto up = a.yt == BL_F32 ? (few ? up_kernel<true, 8>(a.r) : up_kernel<true, 1>(a.r))
-                             : (few ? up_kernel<false, 8>(a.r) : up_kernel<false, 1>(a.r));
+    // rows of whole 16-byte vectors of eight columns
+    const bool vec = a.N % 8 == 0 && aligned(a.y, a.ldy) && aligned(a.out, a.ldo);
+    auto up = a.yt == BL_F32 ? up_kernel<true>(a.r, few, vec) : up_kernel<false>(a.r, few, vec);
     return cuda_status(launch(up, dim3(unsigned(gx), unsigned(std::min<int64_t>(gy, 65535))), kUpWarps * 32, s, p));
 }
 
