@@ -17,6 +17,11 @@ feed-forward activation, and the squared-ReLU gate is this library's
 reading.  Weights are random (seeded, N(0, 0.02^2) absmean-packed); there
 is no tokenizer, embedding or sampling: a decode step maps the residual
 stream of one token through the layers.
+
+A prompt goes through the layers at once (``prefill``): the same layer on the
+many-token kernels (RMSNorm + quantisation, tensor-core GEMMs, rotation with
+cache append, causal attention over the cache), so that decoding continues on
+the caches it leaves.
 """
 from __future__ import annotations
 
@@ -24,8 +29,9 @@ from dataclasses import dataclass, field
 
 import torch
 
-from . import (BL_ACT_PLAIN, BL_ACT_RELU2_GATE, BL_ACT_RMSNORM, attention_decode,
-               attention_workspace, decode_linear, pack, position_advance, rope_table)
+from . import (BL_ACT_PLAIN, BL_ACT_RELU2_GATE, BL_ACT_RMSNORM, BL_ERR_SHAPE, BitLinearError,
+               attention_decode, attention_prefill, attention_workspace, decode_linear, gemm, pack,
+               position_advance, qk_norm_rope, quantize_act, rmsnorm_quantize_act, rope_table)
 
 
 @dataclass
@@ -148,6 +154,43 @@ class Decoder:
         for L in self.layers:
             self.layer_step(L, pdl)
         position_advance(self.pos)
+
+    def prefill(self, x: torch.Tensor, start: int = 0) -> torch.Tensor:
+        """The residual streams x (bf16 [T, hidden]) of the prompt tokens at the
+        positions start .. start + T - 1 through every layer; their keys and
+        values go to those cache rows, behind the rows that earlier pieces of
+        the prompt left.  Returns the streams after the last layer; self.h is
+        the last token's and the position start + T.  A token gets the products
+        that step() gives it, bit for bit where the inputs are; the attention
+        differs in rounding (fp32 sums and bf16 weights, where decoding has
+        fp64).  The gate and the residual sums between the kernels are plain
+        fp32 torch operations."""
+        c = self.cfg
+        T = x.shape[0]
+        if x.dim() != 2 or x.shape[1] != c.hidden or T < 1 or start < 0 or start + T > c.max_seq:
+            raise BitLinearError(BL_ERR_SHAPE, "Decoder.prefill",
+                                 f"x of shape {tuple(x.shape)} at position {start} of {c.max_seq}")
+        D, dev = c.head_dim, x.device
+        positions = torch.arange(start, start + T, dtype=torch.int32, device=dev)
+        # [0, n] without a copy from the host
+        cu_q, cu_k = (torch.arange(0, 2 * n, n, dtype=torch.int32, device=dev) for n in (T, start + T))
+        h = x
+        for L in self.layers:
+            act = rmsnorm_quantize_act(h, L.g_attn, c.eps)
+            q, k, v = (gemm(w, *act).view(T, -1, D) for w in (L.q, L.k, L.v))
+            ck, cv = L.cache_k.transpose(0, 1), L.cache_v.transpose(0, 1)
+            qk_norm_rope(q, k, v, positions, self.scratch["rope"], slots=positions, q_out=q, k_out=ck, v_out=cv)
+            attn = attention_prefill(q, ck, cv, cu_q, cu_k, out=torch.empty_like(q))
+            y = gemm(L.o, *quantize_act(attn.view(T, -1)), out_dtype=torch.float32)
+            h = (h.float() + y).to(torch.bfloat16)
+            act = rmsnorm_quantize_act(h, L.g_ffn, c.eps)
+            gate, up = gemm(L.gate, *act).float(), gemm(L.up, *act).float()
+            gate = gate.relu_().square_().mul_(up)
+            y = gemm(L.down, *quantize_act(gate), out_dtype=torch.float32)
+            h = (h.float() + y).to(torch.bfloat16)
+        self.h.copy_(h[-1])
+        self.set_position(start + T)
+        return h
 
     def weight_bytes(self) -> int:
         return sum(w.packed.numel() for L in self.layers
