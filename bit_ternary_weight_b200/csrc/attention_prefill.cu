@@ -1155,7 +1155,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinSplit = 8;        // CTAs per cut tile, at most
-constexpr int kJoinFew = 8;          // up to so many parts, a warp takes four rows at once
+constexpr int kJoinFew = 8;          // up to so many parts, a warp takes four rows at once,
+constexpr int kJoinRows = 32;        // and where there are more rows than this
 constexpr int kJoinLanes = 8;        // parts per lane: grids of up to 256 CTAs
 
 // A part's share of the sum: 2^(c (m_part - m)) of its l and O.  A part in which
@@ -1178,10 +1179,10 @@ __device__ __forceinline__ void add_part(float4 &acc, float4 o, float f)
 
 // CTA (c, y) takes every gridDim.y-th group of rows of the tile whose first
 // part CTA c of the main kernel holds.  The time is that of a few dependent
-// loads, so many rows go side by side: with few parts (prompts), four rows a
-// warp, whose (m, l) come with one load and whose O's with independent ones;
-// with many (a long cache cut over the GPU), the CTA's warps share a row's
-// parts and add their sums in order.
+// loads, so many rows go side by side: four rows a warp, whose (m, l) come with
+// one load and whose O's with independent ones; where few rows have many parts
+// (single tokens on a long cache), the CTA's warps share a row's parts and add
+// their sums in order.
 template <bool PAIR>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const PrefillParams p)
 {
@@ -1214,36 +1215,43 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
         *reinterpret_cast<uint2 *>(dst + 4 * lane) =
             make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
     };
-    if (parts <= kJoinFew) {
+    if (parts <= kJoinFew || rows > kJoinRows) {
         for (int row0 = (blockIdx.y * kJoinWarps + warp) * 4; row0 < rows; row0 += gridDim.y * kJoinWarps * 4) {
-            // lane 8 r + i: row r, part i
-            const int mine = row0 + lane / 8, i = lane % 8;
-            const bool in = mine < rows && i < parts;
-            const float2 ml = in ? load_ml(i, slot_row(mine)) : make_float2(-INFINITY, 0.0f);
-            float m = ml.x;
+            // lane 8 r + i: row r, parts i, i + 8, ...
+            const int mine = min(row0 + lane / 8, rows - 1), i = lane % 8, my_at = slot_row(mine);
+            auto my_ml = [&](int j0) {
+                return j0 + i < parts ? load_ml(j0 + i, my_at) : make_float2(-INFINITY, 0.0f);
+            };
+            const float2 first = my_ml(0);
+            float m = first.x, l = 0.0f;
+            for (int j0 = 8; j0 < parts; j0 += 8)
+                m = fmaxf(m, my_ml(j0).x);
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1)
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float f = part_factor(ml, m, p.c);
-            float l = ml.y * f;
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1)
-                l += __shfl_xor_sync(0xffffffffu, l, o);
             float4 acc[4] = {};
             int at[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 at[r] = slot_row(min(row0 + r, rows - 1));
+            for (int j0 = 0; j0 < parts; j0 += 8) {
+                const float2 ml = j0 ? my_ml(j0) : first;
+                const float f = part_factor(ml, m, p.c);
+                l = fmaf(ml.y, f, l);
 #pragma unroll 2
-            for (int j = 0; j < parts; ++j) {
-                float4 o[4];
+                for (int j = 0; j < min(8, parts - j0); ++j) {
+                    float4 o[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    o[r] = load_o(j, at[r]);
+                    for (int r = 0; r < 4; ++r)
+                        o[r] = load_o(j0 + j, at[r]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    add_part(acc[r], o[r], __shfl_sync(0xffffffffu, f, 8 * r + j));
+                    for (int r = 0; r < 4; ++r)
+                        add_part(acc[r], o[r], __shfl_sync(0xffffffffu, f, 8 * r + j));
+                }
             }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float lr = __shfl_sync(0xffffffffu, l, 8 * r);
@@ -1347,7 +1355,7 @@ WsLayout ws_layout(int grid)
 
 template <bool PAIR>
 int launch_mode(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const PrefillParams &p, int grid,
-                int64_t q_rows, cudaStream_t s)
+                int64_t q_rows, int64_t k_rows, cudaStream_t s)
 {
     int per_sm = 0;
     int st = occupancy(reinterpret_cast<const void *>(prefill_kernel<PAIR>), kThreads, smem_bytes<PAIR>(), &per_sm);
@@ -1367,6 +1375,9 @@ int launch_mode(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap 
     cfg.numAttrs = 1;       // each kernel waits itself for what came before it
     if ((st = cuda_status(cudaLaunchKernelEx(&cfg, prefill_kernel<PAIR>, qm, km, vm, p))))
         return st;
+    // one block of keys at most for every tile: none is cut
+    if (k_rows <= kKeys)
+        return BL_OK;
     // rows of a tile that there can be, eight warps a CTA
     const int64_t rows = std::min<int64_t>(q_rows, (PAIR ? 2 : 1) * p.TM) * p.G;
     cfg.gridDim = dim3(unsigned(grid), unsigned(std::clamp<int64_t>(rows, 1, kJoinSplit)));
@@ -1414,10 +1425,14 @@ int launch_attention_prefill(const PrefillArgs &a, cudaStream_t s)
     if ((st = make_map(&qm, a.q, a.H, uint32_t(G), uint32_t(p.TM), 1)) ||
         (st = make_map(&km, a.k, a.Hkv, 1, kKeys, 2)) || (st = make_map(&vm, a.v, a.Hkv, 1, kKeys, 2)))
         return st;
-    // two tiles of rows per CTA once every CTA could have a pair of them
+    // Pairs of tiles where there are as many as a quarter of the CTAs and the
+    // sequences have 1 1/4 tiles or more (64 of 48 tokens on 500 others: pair
+    // 54 us, alt 61; 64 of 32: 45 and 42; one of 2048: 43.2 and 44.9; 300 single
+    // tokens on 1000: 176 and 149; one of 256 on 4000, 20 pairs: 32 and 28).
     const int64_t pairs = int64_t(a.Hkv) * (p.Tq / (2 * p.TM));
-    return pairs >= grid / 4 ? launch_mode<true>(qm, km, vm, p, grid, p.Tq, s)
-                             : launch_mode<false>(qm, km, vm, p, grid, p.Tq, s);
+    return pairs >= grid / 4 && 4 * p.Tq >= 5 * int64_t(p.TM) * p.batch
+               ? launch_mode<true>(qm, km, vm, p, grid, p.Tq, p.Tk, s)
+               : launch_mode<false>(qm, km, vm, p, grid, p.Tq, p.Tk, s);
 }
 
 }  // namespace bl
