@@ -366,9 +366,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                 if ((g & 1) != grp)
                     continue;
                 const int s = g % kQStages, a = g % kAStages;
+                // Free before full: the groups take alternate stages of an odd
+                // ring, so a group sees every second phase of full[s] only, and
+                // a wait on its parity alone would also return while the stage
+                // g - kQStages, the other group's, has not landed yet.  The MMAs
+                // of stage g - kAStages are complete here, hence that landed.
+                static_assert(kAStages <= kQStages, "aempty orders the phases of full");
                 // warp-uniform outcomes: the tcgen05.st below is .sync.aligned
-                if (!__all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&sm.full[s]), uint32_t(g / kQStages) & 1u,
-                                                            abort_flag, p.status))) {
+                if (!__all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&sm.aempty[a]), (uint32_t(g / kAStages) & 1u) ^ 1u,
+                                                            abort_flag, p.status) &&
+                                                 mbar_wait_fast(smem_u32(&sm.full[s]), uint32_t(g / kQStages) & 1u,
+                                                                abort_flag, p.status))) {
                     ok = false;
                     break;
                 }
@@ -378,11 +386,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CU
                     const unsigned char *ps = sm.p[s][box] + (rl >> 3) * 256 + (rl & 7) * 16;
                     c4[2 * box] = *reinterpret_cast<const uint4 *>(ps);
                     c4[2 * box + 1] = *reinterpret_cast<const uint4 *>(ps + 128);
-                }
-                if (!__all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&sm.aempty[a]), (uint32_t(g / kAStages) & 1u) ^ 1u,
-                                                            abort_flag, p.status))) {
-                    ok = false;
-                    break;
                 }
                 tc_fence_after();
                 uint32_t v[64];
