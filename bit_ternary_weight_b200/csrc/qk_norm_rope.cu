@@ -147,12 +147,12 @@ struct Raw {
     }
 };
 
-// Norm (NORM) and rotation of every fourth head from `src`, eight lanes a head;
-// `left` heads remain from this group's first on.
+// Norm (NORM) and rotation of every fourth of `heads` heads, from the group's
+// first at `src` on, eight lanes a head.
 //   (a, b) -> (a c1 + b s1, a s2 + b c2) with c1 = g_a c, s1 = -g_b s, s2 = g_a s,
 //   c2 = g_b c, pairs two by two (g = 1 without a norm)
 template <int XT, bool HALVES, bool NORM>
-__device__ __forceinline__ void rotate_heads(const unsigned char *src, __nv_bfloat16 *dst, int64_t ohead, int left,
+__device__ __forceinline__ void rotate_heads(const unsigned char *src, __nv_bfloat16 *dst, int64_t ohead, int heads,
                                              int group, int c, const float2 (&cs)[8], const void *gain, int gt, float eps)
 {
     constexpr int kHeadBytes = kHD * (XT == BL_BF16 ? 2 : 4);
@@ -180,7 +180,7 @@ __device__ __forceinline__ void rotate_heads(const unsigned char *src, __nv_bflo
     }
     const int64_t ostep = 4 * ohead;
 #pragma unroll 2
-    for (int more = left + group; more > 0; more -= 4, src += 4 * kHeadBytes, dst += ostep) {
+    for (int more = heads; more > 0; more -= 4, src += 4 * kHeadBytes, dst += ostep) {
         // a group behind the last head computes on what lies there and stores nothing
         Raw<XT> x;
         x.load(src, c);
@@ -335,11 +335,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 1) qk_norm_rope_kernel(const 
                                   : kind == 1 ? p.ko + row * p.ko_row
                                               : p.vo + row * p.vo_row) + (lo - begin + group) * ohead + 8 * c;
             const unsigned char *src = &sm.slot[warp][slot][(lo - h0 + group) * kHeadBytes];
-            int left = hi - lo - group;         // > 0: this group has a head
             if (kind == 2) {
-                for (; left + group > 0; left -= 4, src += 4 * kHeadBytes, dst += 4 * ohead) {
-                    if (left <= 0)
-                        continue;
+                for (int h = lo + group; h < hi; h += 4, src += 4 * kHeadBytes, dst += 4 * ohead) {
                     Raw<XT> x;
                     x.load(src, c);
                     if constexpr (XT == BL_BF16) {
@@ -361,9 +358,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 1) qk_norm_rope_kernel(const 
             }
             const void *gain = kind ? p.k_gain : p.q_gain;
             if (gain)
-                rotate_heads<XT, HALVES, true>(src, dst, ohead, left, group, c, cs, gain, p.gt, p.eps);
+                rotate_heads<XT, HALVES, true>(src, dst, ohead, hi - lo, group, c, cs, gain, p.gt, p.eps);
             else
-                rotate_heads<XT, HALVES, false>(src, dst, ohead, left, group, c, cs, nullptr, 0, 0.0f);
+                rotate_heads<XT, HALVES, false>(src, dst, ohead, hi - lo, group, c, cs, nullptr, 0, 0.0f);
         }
         __syncwarp();       // every lane has taken its part of the slot
         fetch(item + kRopeSlots * stride, slot);

@@ -159,6 +159,29 @@ def test_long_prompt(bl, H, Hkv, T):
     _check_attention(bl, out, q, k, v, [0, T], [0, T])
 
 
+@pytest.mark.parametrize("H,Hkv,nq,nk", [(7, 1, [1400, 37, 300], None), (6, 2, [1400, 37, 300], None),
+                                         (3, 3, [2500, 1400], None), (20, 5, [400, 300], [1000, 300]),
+                                         (20, 5, [900, 60], [500, 1300]), (16, 2, [333] * 5, [333] * 5),
+                                         (20, 5, [40] * 30, [40] * 30), (64, 1, [50, 90], [50, 800])])
+def test_many_rows(bl, H, Hkv, nq, nk):
+    """Enough rows that two tiles share a pass over the keys: groups that do
+    not divide a tile, tiles that end inside a pair, queries before the keys."""
+    g = _gen(sum(nq) + H)
+    cu_q = _cu(nq)
+    cu_k = _cu(nk or nq)
+    q, k, v = _rand(g, cu_q[-1], H, D), _rand(g, cu_k[-1], Hkv, D, s=1.5), _rand(g, cu_k[-1], Hkv, D)
+    out = bl.attention_prefill(q.to(dev()), k.to(dev()), v.to(dev()), _on_dev(cu_q), _on_dev(cu_k))
+    _check_attention(bl, out, q, k, v, cu_q, cu_k)
+
+
+@pytest.mark.parametrize("H,Hkv,nq,nk", [(20, 5, 130, 9000), (8, 8, 40, 12000), (20, 5, 700, 7000)])
+def test_few_rows_cut_into_many_parts(bl, H, Hkv, nq, nk):
+    g = _gen(nq + nk)
+    q, k, v = _rand(g, nq, H, D), _rand(g, nk, Hkv, D, s=1.5), _rand(g, nk, Hkv, D)
+    out = bl.attention_prefill(q.to(dev()), k.to(dev()), v.to(dev()), _on_dev([0, nq]), _on_dev([0, nk]))
+    _check_attention(bl, out, q, k, v, [0, nq], [0, nk])
+
+
 def test_one_token_on_a_very_long_cache(bl):
     g = _gen(5)
     n = 32768
@@ -402,6 +425,32 @@ def test_rope_without_norm_equals_the_decode_rotation(bl):
         bl.attention_decode(q[t].reshape(-1).to(dev()), k[t].reshape(-1).to(dev()), v[t].reshape(-1).to(dev()), ck, cv,
                             torch.tensor([t], dtype=I32, device=dev()), H, Hkv, table=table)
     assert torch.equal(ck.transpose(0, 1)[:5], ko[:5]) and torch.equal(cv.transpose(0, 1)[:5], vo[:5])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [3, 2500])
+def test_rope_many_heads_and_padded_ones(bl, T, dtype):
+    """More heads than a warp takes at once, heads that do not lie one behind
+    the other, and only keys normed: equal to contiguous single calls."""
+    g = _gen(T)
+    H, Hkv = 64, 8
+    table = bl.rope_table(64, device=dev())
+    pos = (torch.arange(T, dtype=I32) % 64).to(dev())
+    gain = (1 + 0.2 * torch.randn(D, generator=g)).to(dev())
+    wide = torch.randn(T, H + 2 * Hkv, D + 24, generator=g).to(dtype).to(dev())
+    q, k, v = wide[:, :H, 8:D + 8], wide[:, H:H + Hkv, :D], wide[:, H + Hkv:, 16:D + 16]
+    a = bl.qk_norm_rope(q, k, v, pos, table, k_gain=gain)
+    for x, got in ((q, a[0]), (k, a[1])):
+        c = x.contiguous()
+        normed = gain if x is k else None
+        for h in (0, 1, x.shape[1] - 1):
+            one = c[:, h:h + 1].contiguous()
+            want = bl.qk_norm_rope(one, one, None, pos, table, q_gain=normed)[0]
+            assert torch.equal(got[:, h:h + 1], want), h
+    _clean(bl)
+    assert torch.equal(a[2], v.to(BF16))
+    want, size = _rope64(k.cpu(), gain.cpu(), bl.RMS_EPS, table.cpu()[pos.cpu().long()], False)
+    _within(a[1], want, U8 * want.abs() + 16 * U24 * size)
 
 
 def test_rope_in_place_parts_of_a_fused_projection_and_no_values(bl):
