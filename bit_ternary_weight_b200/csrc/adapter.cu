@@ -3,12 +3,14 @@
 //
 // Two launches, the second chained to the first (programmatic dependent
 // launch): u[t] = scale[a] down[a] x[t] in fp32 to the workspace, then
-// out = y + up u.  Both are bound by memory: a token brings 2 r (K + N)
+// out = y + up u; with more than 128 tokens a third before them, which brings
+// tokens of one adapter together.  Both products are bound by memory: a token brings 2 r (K + N)
 // multiply-adds against 2 K + 4 N bytes, and a few tokens bring their whole
 // adapters, so the products run as mma.sync m16n8k16 straight from registers
 // (r columns or r terms are far too few for a tcgen05 tile) and the work is
 // in keeping loads in flight:
-//   - a tile is 16 tokens; the tokens' distinct adapters are found with one
+//   - a tile is 16 tokens (the first launch takes two tiles a CTA where there
+//     are enough); the tokens' distinct adapters are found with one
 //     match across the warp and taken one after the other, each giving only
 //     its own tokens' rows (the other rows of its products are dropped, so
 //     nothing of an adapter reaches a token that does not use it);
@@ -23,6 +25,10 @@
 // u enters the second product as a sum of bf16 values, each the rest of the
 // one before: two (16 bits of it) for bf16 outputs, three (24 bits) for fp32
 // outputs; one alone would cost an output 2^-8 of the adapter's share.
+// Measured (inputs that change from call to call): 4093 tokens of prompts, 2560
+// to 6912 columns, rank 16, 136 MB: 44 us, 3.1 TB/s, of which the order takes 1,
+// the first product 15 and the second 28; 32 tokens of 24 adapters, 2560 x 2560:
+// 11 us, a token at rank 64: 8 us, three to four memory latencies in a row each.
 #include <algorithm>
 
 #include "bl_common.cuh"
@@ -33,6 +39,7 @@ namespace {
 constexpr int kTile = 16;                 // tokens per tile (MMA M)
 constexpr int kDownWarps = 8, kUpWarps = 8;
 constexpr int kUpCols = 32;               // output columns per warp
+constexpr int kChunk = 1024;              // tokens that are sorted together
 
 struct AdapterParams {
     const void *y;
@@ -46,6 +53,7 @@ struct AdapterParams {
     void *out;
     int64_t ldo;
     float *u;                             // [splits][T][r]
+    int2 *order;                          // (token, adapter) in the order of the tiles; null: as they come
     int splits;
     int down_ways;                        // CTAs that share the adapters of a tile
     int *status;
@@ -66,19 +74,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The adapter of token t0 + lane (lanes 0 .. 15), -1: none; an id that does
-// not exist counts as none.
-__device__ __forceinline__ int tile_id(const AdapterParams &p, int64_t t0, int lane, bool report)
+// The adapter of token t, -1: none; an id that does not exist counts as none.
+__device__ __forceinline__ int token_id(const AdapterParams &p, int64_t t, bool report)
 {
-    int id = -1;
-    if (lane < kTile && t0 + lane < p.T)
-        id = int(ld_dep_u32(p.index + t0 + lane));
+    int id = int(ld_dep_u32(p.index + t));
     if (id >= p.n) {
         if (report)
             atomicExch(p.status, BL_ERR_SHAPE);
         id = -1;
     }
     return id < 0 ? -1 : id;
+}
+
+// The token at place `at` of the tiles' order and its adapter.
+__device__ __forceinline__ int2 placed(const AdapterParams &p, int64_t at, bool report)
+{
+    if (!p.order)
+        return make_int2(int(at), token_id(p, at, report));
+    return __ldcg(p.order + at);
 }
 
 // Lanes that are the first with their adapter.
@@ -88,122 +101,202 @@ __device__ __forceinline__ unsigned first_of(int id, int lane)
     return __ballot_sync(0xffffffffu, id >= 0 && lane == __ffs(same) - 1);
 }
 
-// u of one tile, one K split: the warps take the split's 32-k groups in turn
-// and their sums are added through shared memory in a fixed order.
-template <int NT>
-__global__ void __launch_bounds__(kDownWarps * 32) adapter_down_kernel(const AdapterParams p)
+// The order in which tokens go to tiles, for many tokens.  Where tokens of many
+// adapters alternate (requests' single tokens), a tile of consecutive ones takes
+// a product per adapter, up to 16; sorted by adapter within 1024 tokens it takes
+// one or two.  Tokens that come in runs (prompts) stay in place.  A stable
+// counting sort on 255 bins, so the order depends on the ids alone; adapters
+// that share a bin (id mod 255) only share tiles, tokens without one come last.
+// 4096 tokens of 16 adapters, 2560 x 2560, rank 16: 140 -> 31 us with it.
+__global__ void __launch_bounds__(kChunk) adapter_order_kernel(const AdapterParams p)
 {
-    __shared__ float red[kDownWarps / 2][kTile][NT * 8];
+    constexpr int kBins = 256, kWarps = kChunk / 32;
+    __shared__ uint16_t count[kWarps][kBins];     // of a warp's tokens; then what precedes them in the bin
+    __shared__ int base[kBins], warp_sum[kBins / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int e = tid; e < kWarps * kBins / 8; e += kChunk)
+        reinterpret_cast<uint4 *>(&count[0][0])[e] = make_uint4(0, 0, 0, 0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t c0 = int64_t(blockIdx.x) * kChunk, t = c0 + tid;
+    const int id = t < p.T ? token_id(p, t, true) : -1, bin = id < 0 ? kBins - 1 : id % (kBins - 1);
+    const unsigned peers = __match_any_sync(0xffffffffu, bin);
+    const int rank = __popc(peers & ((1u << lane) - 1));
+    // more than four adapters in the warp's two tiles
+    const bool mixed = __popc(__ballot_sync(0xffffffffu, id >= 0 && rank == 0)) > 4;
+    int place = tid;
+    if (__syncthreads_or(mixed)) {
+        if (rank == 0)
+            count[warp][bin] = uint16_t(__popc(peers));
+        __syncthreads();
+        int sum = 0, scan = 0;                    // of bin tid
+        if (tid < kBins) {
+#pragma unroll 8
+            for (int w = 0; w < kWarps; ++w) {
+                const int c = count[w][tid];
+                count[w][tid] = uint16_t(sum);
+                sum += c;
+            }
+            scan = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, scan, o);
+                scan += lane >= o ? v : 0;
+            }
+            if (lane == 31)
+                warp_sum[warp] = scan;
+        }
+        __syncthreads();
+        if (tid < kBins) {
+            for (int w = 0; w < warp; ++w)
+                scan += warp_sum[w];
+            base[tid] = scan - sum;
+        }
+        __syncthreads();
+        place = base[bin] + count[warp][bin] + rank;
+    }
+    // places behind the last token stay there: they are the last of the last bin
+    if (t < p.T)
+        __stcg(p.order + c0 + place, make_int2(int(t), id));
+}
+
+// u of MT tiles, one K split: RW warps side by side have 8 NT ranks each, and
+// 8 / RW take the split's 32-k groups in turn; their sums are added through
+// shared memory in a fixed order.  With many tokens a CTA takes MT = 2 tiles,
+// which share what they read of an adapter: 4096 tokens, 2560 x 2560, rank 64,
+// 59 us instead of 97, rank 16 27 instead of 29 (4 tiles: 33, registers spill).
+template <int NT, int RW, int MT>
+__global__ void __launch_bounds__(kDownWarps * 32, 2) adapter_down_kernel(const AdapterParams p)
+{
+    constexpr int kWays = kDownWarps / RW;                    // warps that share the k groups
+    constexpr int kRows = MT * kTile;
+    static_assert(kRows <= 32, "a lane per row");
+    __shared__ __align__(16) float red[kWays / 2][kRows][RW * NT * 8];
     // the second launch reads y before it waits for this one, so it may begin
     // only when what came before this one is complete
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int64_t t0 = int64_t(blockIdx.x) * kTile;
+    const int64_t t0 = int64_t(blockIdx.x) * kRows;
+    const int valid = int(min(int64_t(kRows), p.T - t0));
     const int way = blockIdx.y, split = blockIdx.z;
-    const int groups = int(p.K / 32);
-    const int k0 = int(int64_t(split) * groups / p.splits) + warp, k1 = int(int64_t(split + 1) * groups / p.splits);
-    constexpr int kDeep = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;      // groups in flight
-    const bool in0 = t0 + g < p.T, in1 = t0 + g + 8 < p.T;
-    const __nv_bfloat16 *x0 = p.x + (t0 + g) * p.ldx + 8 * c, *x1 = x0 + 8 * p.ldx;
+    const int groups = int(p.K / 32), kw = warp / RW, r0 = warp % RW * NT * 8;
+    const int k0 = int(int64_t(split) * groups / p.splits) + kw, k1 = int(int64_t(split + 1) * groups / p.splits);
+    constexpr int kDeep = MT > 1 || NT > 2 ? 2 : 4;           // groups in flight
     const uint4 zero = make_uint4(0, 0, 0, 0);
     // all tokens' x, before their adapters are known: the rows of other
     // adapters are dropped at the end
-    uint4 xa[kDeep], xb[kDeep];
+    int token[MT][2];                                         // -1: behind the last
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m)
+        token[m / 2][m % 2] = 8 * m + g < valid ? int(t0) + 8 * m + g : -1;
+    uint4 x[kDeep][MT][2];
     auto load_x = [&](int k) {
 #pragma unroll
         for (int s = 0; s < kDeep; ++s) {
-            const bool in = k + s * kDownWarps < k1;
-            const int64_t at = int64_t(k + s * kDownWarps) * 32;
-            xa[s] = in && in0 ? ld_dep_v4(x0 + at) : zero;
-            xb[s] = in && in1 ? ld_dep_v4(x1 + at) : zero;
+            const __nv_bfloat16 *at = p.x + int64_t(k + s * kWays) * 32 + 8 * c;
+#pragma unroll
+            for (int m = 0; m < 2 * MT; ++m) {
+                const int t = token[m / 2][m % 2];
+                x[s][m / 2][m % 2] = k + s * kWays < k1 && t >= 0 ? ld_dep_v4(at + t * p.ldx) : zero;
+            }
         }
     };
     load_x(k0);
-    const bool once = k0 + kDeep * kDownWarps >= k1;          // that was all of it
-    const int id = tile_id(p, t0, lane, way == 0 && split == 0);
+    const int2 mine = lane < valid ? placed(p, t0 + lane, way == 0 && split == 0) : make_int2(-1, -1);
+    if (p.order) {
+        // and again where other tokens than the consecutive ones are the tiles'
+        bool moved = false;
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) {
+            const int t = __shfl_sync(0xffffffffu, mine.x, 8 * m + g);
+            moved |= t != token[m / 2][m % 2];
+            token[m / 2][m % 2] = t;
+        }
+        if (__any_sync(0xffffffffu, moved))
+            load_x(k0);
+    }
+    int held = k0;                                            // x of the groups from here on is in registers
+    const int id = mine.y;
     unsigned firsts = first_of(id, lane);
     for (int ord = 0; firsts; ++ord, firsts &= firsts - 1) {
         if (ord % p.down_ways != way)
             continue;
         const int a = __shfl_sync(0xffffffffu, id, __ffs(firsts) - 1);
         const unsigned rows = __ballot_sync(0xffffffffu, id == a);
-        const __nv_bfloat16 *w = p.down + (int64_t(a) * p.r + g) * p.K + 8 * c;
-        float acc[NT][4] = {};
-        for (int k = k0; k < k1; k += kDeep * kDownWarps) {
+        const __nv_bfloat16 *w = p.down + (int64_t(a) * p.r + r0 + g) * p.K + 8 * c;
+        float acc[MT][NT][4] = {};
+        for (int k = k0; k < k1; k += kDeep * kWays) {
             uint4 b[kDeep][NT];
-            if (!once)
-                load_x(k);
+            if (k != held)
+                load_x(held = k);
 #pragma unroll
             for (int s = 0; s < kDeep; ++s) {
-                const int64_t at = int64_t(k + s * kDownWarps) * 32;
+                const int64_t at = int64_t(k + s * kWays) * 32;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    b[s][j] = k + s * kDownWarps < k1 && j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
+                    b[s][j] = k + s * kWays < k1 && r0 + j * 8 < p.r ? ld_ro_v4(w + j * 8 * p.K + at) : zero;
             }
 #pragma unroll
             for (int s = 0; s < kDeep; ++s) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    mma_bf16(acc[j], xa[s].x, xb[s].x, xa[s].y, xb[s].y, b[s][j].x, b[s][j].y);
-                    mma_bf16(acc[j], xa[s].z, xb[s].z, xa[s].w, xb[s].w, b[s][j].z, b[s][j].w);
+                for (int m = 0; m < MT; ++m) {
+                    const uint4 xa = x[s][m][0], xb = x[s][m][1];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        mma_bf16(acc[m][j], xa.x, xb.x, xa.y, xb.y, b[s][j].x, b[s][j].y);
+                        mma_bf16(acc[m][j], xa.z, xb.z, xa.w, xb.w, b[s][j].z, b[s][j].w);
+                    }
                 }
             }
         }
-        // sums of warps w and w + 4, then of the four pairs
-        const int pair = warp & (kDownWarps / 2 - 1);
+        // sums of the first and the second half of the k ways, then of all pairs
+        const int pair = kw % (kWays / 2);
         for (int half = 1; half >= 0; --half) {
-            if (warp / (kDownWarps / 2) == half) {
+            if (kw / (kWays / 2) == half) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
+                for (int m = 0; m < MT; ++m) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float &s = red[pair][g + 8 * (e >> 1)][8 * j + 2 * c + (e & 1)];
-                        s = half ? acc[j][e] : s + acc[j][e];
+                    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            float2 &s = *reinterpret_cast<float2 *>(&red[pair][16 * m + g + 4 * e][r0 + 8 * j + 2 * c]);
+                            const float2 v = make_float2(acc[m][j][e], acc[m][j][e + 1]);
+                            s = half ? v : make_float2(s.x + v.x, s.y + v.y);
+                        }
                     }
                 }
             }
             __syncthreads();
         }
         const float scale = p.scale ? __ldcg(p.scale + a) : 1.0f;
-        for (int e = threadIdx.x; e < kTile * p.r; e += kDownWarps * 32) {
-            const int row = e / p.r, j = e - row * p.r;
-            if (rows >> row & 1) {
-                float s = red[0][row][j];
+        const int fours = p.r / 4;
+        for (int e = threadIdx.x; e < kRows * fours; e += kDownWarps * 32) {
+            const int at = e / fours, j = 4 * (e - at * fours);
+            if (rows >> at & 1) {
+                float4 s = *reinterpret_cast<const float4 *>(&red[0][at][j]);
 #pragma unroll
-                for (int q = 1; q < kDownWarps / 2; ++q)
-                    s += red[q][row][j];
-                __stcg(p.u + (int64_t(split) * p.T + t0 + row) * p.r + j, s * scale);
+                for (int q = 1; q < kWays / 2; ++q) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&red[q][at][j]);
+                    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+                }
+                __stcg(reinterpret_cast<float4 *>(p.u + (int64_t(split) * p.T + t0 + at) * p.r + j),
+                       make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale));
             }
         }
         __syncthreads();
     }
 }
 
-// Eight consecutive elements of a row, as loaded: 16-byte vectors (VEC), or one
-// element after the other where rows are not aligned or end inside the eight
-// (`left` of them are there).
-template <bool F32, bool VEC>
+// Eight consecutive elements of a row of whole 16-byte vectors.
+template <bool F32>
 struct Cols {
     uint4 v[F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const char *src, int64_t left)
+    __device__ __forceinline__ void load(const char *src)
     {
-        if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < (F32 ? 2 : 1); ++i)
-                v[i] = ld_dep_v4(src + 16 * i);
-        } else {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i] = i >= left ? 0u : F32 ? ld_dep_u32(src + 4 * i) : ld_dep_u16(src + 2 * i);
-            if constexpr (F32) {
-                v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                v[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            } else {
-                v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-            }
-        }
+        for (int i = 0; i < (F32 ? 2 : 1); ++i)
+            v[i] = ld_dep_v4(src + 16 * i);
     }
     __device__ __forceinline__ void floats(float (&f)[8]) const
     {
@@ -223,19 +316,14 @@ struct Cols {
             }
         }
     }
-    static __device__ __forceinline__ void store(char *dst, const float (&f)[8], int64_t left)
+    static __device__ __forceinline__ void store(char *dst, const float (&f)[8])
     {
-        if constexpr (VEC && F32) {
+        if constexpr (F32) {
             reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
             reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else if constexpr (VEC) {
+        } else {
             *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
                                                          pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left)
-                    store_y(dst, F32 ? BL_F32 : BL_BF16, i, f[i]);
         }
     }
 };
@@ -252,73 +340,94 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[TERMS
     }
 }
 
-// out = y + up u for runs of tiles and the columns of a CTA.  A warp has 32
-// columns; WAYS = 1: the warps of a CTA lie side by side and take a run's
+// out = y + up u for runs of TILES tiles and the columns of a CTA.  A warp has
+// 32 columns; WAYS = 1: the warps of a CTA lie side by side and take a run's
 // tiles one after the other, every tile's y in flight from the start; WAYS = 8:
 // they share 32 columns and the adapters of one tile.  y and the adapters are
 // asked for while the first launch still runs.  u, the K splits' parts added
 // in order, is split into its bf16 terms once per CTA, and a tile whose tokens
 // share one adapter (most tiles of a prompt) keeps its operand from tile to
 // tile and starts the accumulators at y (bf16 outputs; an fp32 output adds y at
-// the end, since a tensor core's sums lose up to 2^-23 of y each).
-template <int KB, bool F32, int WAYS, bool VEC>
+// the end, since a tensor core's sums lose up to 2^-23 of y each).  Rows that
+// are not whole 16-byte vectors (VEC = false) go through shared memory, so
+// that a warp reads and writes 32 columns of a row at once: 4096 tokens, 704 x
+// 1001, rank 16, 26 us instead of 35 with a lane's eight columns one by one.
+template <int KB, bool F32, int WAYS, int TILES, bool VEC>
 __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const AdapterParams p)
 {
-    constexpr int kTiles = WAYS == 1 ? (F32 ? 2 : 4) : 1;
-    constexpr int kTokens = kTiles * kTile;
+    static_assert(VEC || TILES == 1, "rows through shared memory: a tile at a time");
+    constexpr int kTokens = TILES * kTile;
     constexpr int kTerms = F32 ? 3 : 2;
     constexpr int kPitch = 8 * KB + 4;                        // words (two ranks) per token
     __shared__ uint32_t u_s[kTerms][kTokens][kPitch];
-    __shared__ int id_s[kTokens];
+    __shared__ int id_s[kTokens], token_s[kTokens];
+    __shared__ float2 sums[VEC ? 1 : kUpWarps][kTile][VEC ? 1 : kUpCols / 2 + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int way = WAYS == 1 ? 0 : warp;
     const int64_t n0 = (int64_t(blockIdx.x) * (kUpWarps / WAYS) + (WAYS == 1 ? warp : 0)) * kUpCols;
     const int64_t nc = n0 + 8 * c;                            // this lane's output columns
-    const int64_t left = p.N - nc;                            // columns from there to the row's end
-    const bool cols = n0 < p.N;
+    const bool cols = n0 < p.N, own = nc < p.N;
     constexpr int kElem = F32 ? 4 : 2;
-    using Eight = Cols<F32, VEC>;
+    const char *const yp = static_cast<const char *>(p.y);
+    char *const op = static_cast<char *>(p.out);
     bool waited = false;
-    constexpr int kKept = KB <= 2 ? KB : 1;                   // k blocks of an adapter's operand in registers
-    uint2 b[kKept][4];
-    int b_of = -1;                                            // the adapter that b holds (KB <= 2)
-    auto load_kb = [&](int a, int kb, uint2 (&v)[4]) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            // column g of tile x: 8 (g / 2) + 2 x + g % 2; this lane's four ranks
-            const int64_t n = n0 + 8 * (g >> 1) + 2 * x + (g & 1);
-            const int k = 16 * kb + 4 * c;
-            v[x] = make_uint2(0, 0);
-            if (k < p.r && n < p.N)
-                v[x] = __ldg(reinterpret_cast<const uint2 *>(p.up + (int64_t(a) * p.N + n) * p.r + k));
-        }
-    };
+    uint2 b[KB][4];
+    int b_of = -1;                                            // the adapter that b holds
     auto load_b = [&](int a) {
-        if (KB > 2 || a == b_of)
+        if (a == b_of)
             return;
         b_of = a;
 #pragma unroll
-        for (int kb = 0; kb < kKept; ++kb)
-            load_kb(a, kb, b[kb]);
+        for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                // column g of tile x: 8 (g / 2) + 2 x + g % 2; this lane's four ranks
+                const int64_t n = n0 + 8 * (g >> 1) + 2 * x + (g & 1);
+                const int k = 16 * kb + 4 * c;
+                b[kb][x] = make_uint2(0, 0);
+                if (k < p.r && n < p.N)
+                    b[kb][x] = __ldg(reinterpret_cast<const uint2 *>(p.up + (int64_t(a) * p.N + n) * p.r + k));
+            }
+        }
     };
     for (int64_t run = blockIdx.y; run * kTokens < p.T; run += gridDim.y) {
         const int64_t t0 = run * kTokens;
         const int tokens = int(min(int64_t(kTokens), p.T - t0));
         __syncthreads();                                      // the last run's u has been used
-        Eight y[kTiles][2];
-        {
-            const char *src = static_cast<const char *>(p.y) + ((t0 + g) * p.ldy + nc) * kElem;
+        Cols<F32> y[TILES][2];
+        if constexpr (VEC) {
+            const char *src = yp + ((t0 + g) * p.ldy + nc) * kElem;
             const int64_t step = 8 * p.ldy * kElem;
 #pragma unroll
-            for (int i = 0; i < 2 * kTiles; ++i, src += step)
-                if (8 * i + g < tokens && left > 0)
-                    y[i / 2][i % 2].load(src, left);
+            for (int i = 0; i < 2 * TILES; ++i, src += step)
+                if (8 * i + g < tokens && own)
+                    y[i / 2][i % 2].load(src);
         }
+        bool moved = false;
         if (threadIdx.x < kTokens) {
-            const int id = int(threadIdx.x) < tokens ? int(ld_dep_u32(p.index + t0 + threadIdx.x)) : -1;
-            id_s[threadIdx.x] = id < 0 || id >= p.n ? -1 : id;     // reported by the first launch
+            const int2 at = int(threadIdx.x) < tokens ? placed(p, t0 + threadIdx.x, false) : make_int2(0, -1);
+            token_s[threadIdx.x] = at.x;
+            id_s[threadIdx.x] = at.y;
+            moved = int(threadIdx.x) < tokens && at.x != t0 + threadIdx.x;
         }
-        __syncthreads();
+        moved = __syncthreads_or(moved);
+        if constexpr (VEC) {
+            // again where other tokens than the consecutive ones are the run's
+            if (moved) {
+#pragma unroll
+                for (int i = 0; i < 2 * TILES; ++i)
+                    if (8 * i + g < tokens && own)
+                        y[i / 2][i % 2].load(yp + (token_s[8 * i + g] * p.ldy + nc) * kElem);
+            }
+        }
+        uint32_t w[kTile];                                    // column n0 + lane of the rows (VEC = false)
+        if constexpr (!VEC) {
+#pragma unroll
+            for (int r = 0; r < kTile; ++r) {
+                const char *src = yp + (token_s[r] * p.ldy + n0 + lane) * kElem;
+                w[r] = r >= tokens || n0 + lane >= p.N ? 0u : F32 ? ld_dep_u32(src) : ld_dep_u16(src) << 16;
+            }
+        }
         if (WAYS == 1 && cols && id_s[0] >= 0)
             load_b(id_s[0]);
         if (!waited) {
@@ -347,10 +456,8 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
         __syncthreads();
         if (!cols)
             continue;
-        char *dst = static_cast<char *>(p.out) + ((t0 + g) * p.ldo + nc) * kElem;
-        const int64_t ostep = 8 * p.ldo * kElem;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i, dst += 2 * ostep) {
+        for (int i = 0; i < TILES; ++i) {
             if (16 * i >= tokens)
                 break;
             // acc += up u of adapter a for all 16 tokens (rows of other
@@ -361,89 +468,126 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
                 for (int kb = 0; kb < KB; ++kb) {
                     if (16 * kb >= p.r)
                         break;
-                    if (KB > 2)
-                        load_kb(a, kb, b[0]);
-                    uint2 (&bk)[4] = b[KB > 2 ? 0 : kb];
 #pragma unroll
                     for (int q = kTerms - 1; q >= 0; --q) {
                         const uint2 ua = *reinterpret_cast<const uint2 *>(&u_s[q][16 * i + g][8 * kb + 2 * c]);
                         const uint2 ub = *reinterpret_cast<const uint2 *>(&u_s[q][16 * i + g + 8][8 * kb + 2 * c]);
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            mma_bf16(acc[x], ua.x, ub.x, ua.y, ub.y, bk[x].x, bk[x].y);
+                            mma_bf16(acc[x], ua.x, ub.x, ua.y, ub.y, b[kb][x].x, b[kb][x].y);
                     }
                 }
             };
+            auto dst = [&](int h) { return op + (token_s[16 * i + 8 * h + g] * p.ldo + nc) * kElem; };
             const int id = lane < kTile ? id_s[16 * i + lane] : -1;
             const int valid = min(16, tokens - 16 * i), one = __shfl_sync(0xffffffffu, id, 0);
-            if (!F32 && WAYS == 1 && one >= 0 && __all_sync(0xffffffffu, id == one || lane >= valid)) {
-                float acc[4][4], f[8];
+            if constexpr (VEC && !F32 && WAYS == 1) {
+                if (one >= 0 && __all_sync(0xffffffffu, id == one || lane >= valid)) {
+                    float acc[4][4], f[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    y[i][h].floats(f);
+                    for (int h = 0; h < 2; ++h) {
+                        y[i][h].floats(f);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        acc[x][2 * h] = f[2 * x];
-                        acc[x][2 * h + 1] = f[2 * x + 1];
+                        for (int x = 0; x < 4; ++x) {
+                            acc[x][2 * h] = f[2 * x];
+                            acc[x][2 * h + 1] = f[2 * x + 1];
+                        }
                     }
-                }
-                product(one, acc);
+                    product(one, acc);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        f[2 * x] = acc[x][2 * h];
-                        f[2 * x + 1] = acc[x][2 * h + 1];
+                        for (int x = 0; x < 4; ++x) {
+                            f[2 * x] = acc[x][2 * h];
+                            f[2 * x + 1] = acc[x][2 * h + 1];
+                        }
+                        if (g + 8 * h < valid && own)
+                            Cols<F32>::store(dst(h), f);
                     }
-                    if (g + 8 * h < valid && left > 0)
-                        Eight::store(dst + h * ostep, f, left);
+                    continue;
                 }
-                continue;
             }
+            // out = y + the product with adapter a (-1: y) for some of the tile's rows
+            auto finish = [&](unsigned rows, int a) {
+                float acc[4][4] = {};
+                if constexpr (VEC) {
+                    if (a >= 0)
+                        product(a, acc);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if ((rows >> (g + 8 * h) & 1) && own) {
+                            float f[8];
+                            y[i][h].floats(f);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                f[2 * x] += acc[x][2 * h];
+                                f[2 * x + 1] += acc[x][2 * h + 1];
+                            }
+                            Cols<F32>::store(dst(h), f);
+                        }
+                    }
+                } else {
+                    const int64_t n = n0 + lane;
+                    rows = n < p.N ? rows : 0;
+                    if (a >= 0)
+                        product(a, acc);
+                    __syncwarp();                             // the last sums have been read
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            sums[warp][g + 8 * h][4 * c + x] = make_float2(acc[x][2 * h], acc[x][2 * h + 1]);
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < kTile; ++r)
+                        if (rows >> r & 1)
+                            store_y(op + token_s[r] * p.ldo * kElem, F32 ? BL_F32 : BL_BF16, n,
+                                    __uint_as_float(w[r]) + reinterpret_cast<const float *>(sums[warp][r])[lane]);
+                }
+            };
             unsigned firsts = first_of(id, lane);
             const unsigned none = __ballot_sync(0xffffffffu, lane < valid && id < 0);
-            if (way == 0) {                                   // tokens without an adapter
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if ((none >> (g + 8 * h) & 1) && left > 0) {
-                        float f[8];
-                        y[i][h].floats(f);
-                        Eight::store(dst + h * ostep, f, left);
-                    }
-                }
-            }
+            if (way == 0 && none)
+                finish(none, -1);
             for (int ord = 0; firsts; ++ord, firsts &= firsts - 1) {
                 if (WAYS > 1 && ord % WAYS != way)
                     continue;
                 const int a = __shfl_sync(0xffffffffu, id, __ffs(firsts) - 1);
-                const unsigned rows = __ballot_sync(0xffffffffu, id == a);
-                float acc[4][4] = {};
-                product(a, acc);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if ((rows >> (g + 8 * h) & 1) && left > 0) {
-                        float f[8];
-                        y[i][h].floats(f);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            f[2 * x] += acc[x][2 * h];
-                            f[2 * x + 1] += acc[x][2 * h + 1];
-                        }
-                        Eight::store(dst + h * ostep, f, left);
-                    }
-                }
+                finish(__ballot_sync(0xffffffffu, id == a), a);
             }
         }
     }
 }
 
-// K splits of the first launch: six CTAs per SM (a warp's groups are then in
-// flight at once) while each warp still has a 32-k group (K >= 64; T is all the workspace's size may depend on, so
-// the splits go by the tokens and the launch takes no more than K allows).
+// Tiles of a run: as many as leave the adapter's operand (8 KB registers) and
+// the tiles' y in registers.
+constexpr int run_tiles(int kb, bool f32) { return kb > 4 ? 1 : kb > 2 ? (f32 ? 1 : 2) : f32 ? 2 : 4; }
+
+// With fewer tokens, the adapters of a tile have warps and CTAs of their own.
+constexpr int64_t kOrderTokens = 128;
+
+// K splits of the first launch at most: eight CTAs of a tile, or two of two
+// tiles, per SM (T is all the workspace's size may depend on).
 int max_splits(int64_t T, int sms)
 {
     const int64_t tiles = (T + kTile - 1) / kTile;
-    return int(std::clamp<int64_t>(6 * sms / tiles, 1, 32));
+    return int(std::clamp<int64_t>(8 * sms / tiles, 1, 32));
+}
+
+// One tile a CTA or two.
+auto down_kernel(int r, bool two) -> void (*)(AdapterParams)
+{
+    if (two)
+        return r <= 8    ? adapter_down_kernel<1, 1, 2>
+               : r <= 16 ? adapter_down_kernel<2, 1, 2>
+               : r <= 32 ? adapter_down_kernel<4, 1, 2>
+               : r <= 64 ? adapter_down_kernel<4, 2, 2>
+                         : adapter_down_kernel<4, 4, 2>;
+    return r <= 8    ? adapter_down_kernel<1, 1, 1>
+           : r <= 16 ? adapter_down_kernel<2, 1, 1>
+           : r <= 32 ? adapter_down_kernel<4, 1, 1>
+           : r <= 64 ? adapter_down_kernel<4, 2, 1>
+                     : adapter_down_kernel<4, 4, 1>;
 }
 
 cudaError_t launch(void (*kernel)(AdapterParams), dim3 grid, int threads, cudaStream_t s, const AdapterParams &p)
@@ -460,20 +604,25 @@ cudaError_t launch(void (*kernel)(AdapterParams), dim3 grid, int threads, cudaSt
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <bool F32, int WAYS, bool VEC>
-auto up_kernel(int r) -> void (*)(AdapterParams)
+enum class Up { kFew, kTile, kRun };      // eight warps a tile; a tile, a run of tiles a warp
+
+template <int KB, bool F32>
+auto up_kernel(Up kind, bool vec) -> void (*)(AdapterParams)
 {
-    return r <= 16   ? adapter_up_kernel<1, F32, WAYS, VEC>
-           : r <= 32 ? adapter_up_kernel<2, F32, WAYS, VEC>
-           : r <= 64 ? adapter_up_kernel<4, F32, WAYS, VEC>
-                     : adapter_up_kernel<8, F32, WAYS, VEC>;
+    if (kind == Up::kFew)
+        return vec ? adapter_up_kernel<KB, F32, 8, 1, true> : adapter_up_kernel<KB, F32, 8, 1, false>;
+    return !vec                 ? adapter_up_kernel<KB, F32, 1, 1, false>
+           : kind == Up::kTile ? adapter_up_kernel<KB, F32, 1, 1, true>
+                               : adapter_up_kernel<KB, F32, 1, run_tiles(KB, F32), true>;
 }
 
 template <bool F32>
-auto up_kernel(int r, bool few, bool vec) -> void (*)(AdapterParams)
+auto up_kernel(int r, Up kind, bool vec) -> void (*)(AdapterParams)
 {
-    return few ? (vec ? up_kernel<F32, 8, true>(r) : up_kernel<F32, 8, false>(r))
-               : (vec ? up_kernel<F32, 1, true>(r) : up_kernel<F32, 1, false>(r));
+    return r <= 16   ? up_kernel<1, F32>(kind, vec)
+           : r <= 32 ? up_kernel<2, F32>(kind, vec)
+           : r <= 64 ? up_kernel<4, F32>(kind, vec)
+                     : up_kernel<8, F32>(kind, vec);
 }
 
 }  // namespace
@@ -481,7 +630,9 @@ auto up_kernel(int r, bool few, bool vec) -> void (*)(AdapterParams)
 size_t adapter_workspace_bytes(int64_t T, int r)
 {
     const DeviceInfo *di = device_info();
-    return di ? size_t(max_splits(T, di->sm_count)) * size_t(T) * size_t(r) * sizeof(float) : 0;
+    return di ? size_t(max_splits(T, di->sm_count)) * size_t(T) * size_t(r) * sizeof(float) +
+                    (T > kOrderTokens ? size_t(T) * sizeof(int2) : 0)
+              : 0;
 }
 
 int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
@@ -509,26 +660,40 @@ int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)
     p.out = a.out;
     p.ldo = a.ldo;
     p.u = static_cast<float *>(a.ws);
-    p.splits = int(std::clamp<int64_t>(a.K / 32 / kDownWarps, 1, max_splits(a.T, di->sm_count)));
+    // two tiles a CTA where those and the K splits (of a group a warp or more) fill the GPU
+    const int64_t pairs = (tiles + 1) / 2, k_splits = a.K / 32 / kDownWarps;
+    const bool two = pairs * std::min<int64_t>(k_splits, max_splits(a.T, di->sm_count)) >= di->sm_count;
+    p.splits = int(std::clamp<int64_t>(two ? 2 * di->sm_count / pairs : 6 * di->sm_count / tiles, 1,
+                                       std::clamp<int64_t>(k_splits, 1, max_splits(a.T, di->sm_count))));
     p.status = di->status;
+    const bool ordered = a.T > kOrderTokens && a.n > 1;
     // a tile's adapters go to CTAs of their own while tiles alone do not fill the GPU
-    p.down_ways = int(std::clamp<int64_t>(di->sm_count / tiles, 1, std::min<int64_t>({kTile, a.n, a.T})));
-    auto down = a.r <= 8    ? adapter_down_kernel<1>
-                : a.r <= 16 ? adapter_down_kernel<2>
-                : a.r <= 32 ? adapter_down_kernel<4>
-                : a.r <= 64 ? adapter_down_kernel<8>
-                            : adapter_down_kernel<16>;
-    const dim3 dgrid(unsigned(tiles), unsigned(p.down_ways), unsigned(p.splits));
-    int st = cuda_status(launch(down, dgrid, kDownWarps * 32, s, p));
+    p.down_ways = int(std::clamp<int64_t>(di->sm_count / tiles, 1, std::min<int64_t>({ordered ? 2 : kTile, a.n, a.T})));
+    auto down = down_kernel(a.r, two);
+    int st = BL_OK;
+    if (ordered) {
+        // behind u, whose size is a multiple of 16 bytes
+        p.order = reinterpret_cast<int2 *>(p.u + size_t(max_splits(a.T, di->sm_count)) * a.T * a.r);
+        st = cuda_status(launch(adapter_order_kernel, dim3(unsigned((a.T + kChunk - 1) / kChunk)), kChunk, s, p));
+        if (st)
+            return st;
+    }
+    const dim3 dgrid(unsigned(two ? pairs : tiles), unsigned(p.down_ways), unsigned(p.splits));
+    st = cuda_status(launch(down, dgrid, kDownWarps * 32, s, p));
     if (st)
         return st;
-    // few tokens: a CTA per 32 columns and 16 tokens, its warps share the adapters
-    const bool few = tiles * ((a.N + 8 * kUpCols - 1) / (8 * kUpCols)) < 2 * di->sm_count;
-    const int cols = few ? kUpCols : kUpWarps * kUpCols, tokens = kTile * (few ? 1 : a.yt == BL_F32 ? 2 : 4);
-    const int64_t gx = (a.N + cols - 1) / cols, gy = (a.T + tokens - 1) / tokens;
     // rows of whole 16-byte vectors of eight columns
-    const bool vec = a.N % 8 == 0 && aligned(a.y, a.ldy) && aligned(a.out, a.ldo);
-    auto up = a.yt == BL_F32 ? up_kernel<true>(a.r, few, vec) : up_kernel<false>(a.r, few, vec);
+    const bool vec = a.N % 8 == 0 && aligned(a.y, a.ldy) && aligned(a.out, a.ldo), f32 = a.yt == BL_F32;
+    // few tokens: a CTA per 32 columns and tile, its warps share the adapters;
+    // else 256 columns, and a run of tiles where runs fill the GPU
+    const int64_t wide = (a.N + kUpWarps * kUpCols - 1) / (kUpWarps * kUpCols);
+    const int run = vec ? run_tiles(a.r <= 32 ? 2 : a.r <= 64 ? 4 : 8, f32) : 1;
+    const Up kind = a.T <= kOrderTokens && tiles * wide < 2 * di->sm_count ? Up::kFew
+                    : tiles * wide < run * di->sm_count                    ? Up::kTile
+                                                                           : Up::kRun;
+    const int64_t gx = kind == Up::kFew ? (a.N + kUpCols - 1) / kUpCols : wide;
+    const int64_t gy = kind == Up::kRun ? (tiles + run - 1) / run : tiles;
+    auto up = f32 ? up_kernel<true>(a.r, kind, vec) : up_kernel<false>(a.r, kind, vec);
     return cuda_status(launch(up, dim3(unsigned(gx), unsigned(std::min<int64_t>(gy, 65535))), kUpWarps * 32, s, p));
 }
 

@@ -585,6 +585,35 @@ def test_adapter_add(bl, T, K, N, r, n, dtype, order):
     _check_adapter(bl, got, y, x, down, up, index, scale)
 
 
+@pytest.mark.parametrize("T,K,N,r,n", [(129, 2560, 264, 128, 9), (1025, 320, 1001, 64, 5), (2100, 256, 200, 16, 600),
+                                       (4100, 64, 72, 8, 300), (1500, 2560, 130, 40, 20)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_adapter_of_many_alternating_requests(bl, T, K, N, r, n, dtype):
+    """Tokens of many requests side by side, more adapters than are told apart
+    when tokens are brought together; in place, ids that do not exist among
+    them, and once more with other ids through the same graph."""
+    g = _gen(T + r)
+    x, y = _rand(g, T, K), torch.randn(T, N, generator=g).to(dtype)
+    down, up = _rand(g, n, r, K, s=K ** -0.5), _rand(g, n, N, r, s=r ** -0.5)
+    scale = 0.5 + torch.rand(n, generator=g)
+    ids = [torch.randint(-1, n, (T,), generator=g).to(I32), torch.randint(-2, n, (T,), generator=g).to(I32)]
+    ids[0][40:80] = n - 1
+    out, index = y.to(dev()), ids[0].to(dev())
+    xd, dd, ud, sd = x.to(dev()), down.to(dev()), up.to(dev()), scale.to(dev())
+    bl.adapter_add(out, xd, dd, ud, index, scale=sd, out=out)
+    _check_adapter(bl, out, y, x, down, up, ids[0], scale)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bl.adapter_add(out, xd, dd, ud, index, scale=sd, out=out)
+    for i in (0, 1):
+        index.copy_(ids[i])
+        out.copy_(y)
+        graph.replay()
+        _check_adapter(bl, out, y, x, down, up, ids[i], scale)
+    again = bl.adapter_add(y.to(dev()), xd, dd, ud, index, scale=sd)
+    assert torch.equal(again, out)
+
+
 def test_adapter_prompt(bl):
     g = _gen(61)
     T, K, N, r, n = 1500, 2560, 640, 16, 4
