@@ -345,10 +345,11 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[TERMS
 // tiles one after the other, every tile's y in flight from the start; WAYS = 8:
 // they share 32 columns and the adapters of one tile.  y and the adapters are
 // asked for while the first launch still runs.  u, the K splits' parts added
-// in order, is split into its bf16 terms once per CTA, and a tile whose tokens
-// share one adapter (most tiles of a prompt) keeps its operand from tile to
-// tile and starts the accumulators at y (bf16 outputs; an fp32 output adds y at
-// the end, since a tensor core's sums lose up to 2^-23 of y each).  Rows that
+// in order, is split into its bf16 terms once per CTA, and the operand of the
+// last adapter stays from tile to tile (prompts).  The accumulators start at y
+// (bf16 outputs; an fp32 output adds y at the end, since a tensor core's sums
+// lose up to 2^-23 of y each), whichever tokens share the tile, so that a token
+// gets the same bits beside any others where the K splits are the same.  Rows that
 // are not whole 16-byte vectors (VEC = false) go through shared memory, so
 // that a warp reads and writes 32 columns of a row at once: 4096 tokens, 704 x
 // 1001, rank 16, 26 us instead of 35 with a lane's eight columns one by one.
@@ -482,25 +483,23 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
             const int id = lane < kTile ? id_s[16 * i + lane] : -1;
             const int valid = min(16, tokens - 16 * i), one = __shfl_sync(0xffffffffu, id, 0);
             if constexpr (VEC && !F32 && WAYS == 1) {
+                // one adapter for all (most tiles of a prompt): what finish() does,
+                // without its loop and masks (48.7 us of prompts without this)
                 if (one >= 0 && __all_sync(0xffffffffu, id == one || lane >= valid)) {
                     float acc[4][4], f[8];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         y[i][h].floats(f);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            acc[x][2 * h] = f[2 * x];
-                            acc[x][2 * h + 1] = f[2 * x + 1];
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            acc[e / 2][2 * h + e % 2] = f[e];
                     }
                     product(one, acc);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            f[2 * x] = acc[x][2 * h];
-                            f[2 * x + 1] = acc[x][2 * h + 1];
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = acc[e / 2][2 * h + e % 2];
                         if (g + 8 * h < valid && own)
                             Cols<F32>::store(dst(h), f);
                     }
@@ -511,19 +510,25 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
             auto finish = [&](unsigned rows, int a) {
                 float acc[4][4] = {};
                 if constexpr (VEC) {
+                    float f[2][8];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        y[i][h].floats(f[h]);
+                        if constexpr (!F32) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                acc[e / 2][2 * h + e % 2] = f[h][e];
+                        }
+                    }
                     if (a >= 0)
                         product(a, acc);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if ((rows >> (g + 8 * h) & 1) && own) {
-                            float f[8];
-                            y[i][h].floats(f);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                f[2 * x] += acc[x][2 * h];
-                                f[2 * x + 1] += acc[x][2 * h + 1];
-                            }
-                            Cols<F32>::store(dst(h), f);
+                            for (int e = 0; e < 8; ++e)
+                                f[h][e] = acc[e / 2][2 * h + e % 2] + (F32 ? f[h][e] : 0.0f);
+                            Cols<F32>::store(dst(h), f[h]);
                         }
                     }
                 } else {
