@@ -44,6 +44,13 @@
 //                   product (a zero weight times a NaN would reach rows that
 //                   do not see it) and rows that do see them get NaN.
 //
+// Measured (20 + 5 heads, with the join): a prompt of 8192 303 us, 1.13 PFLOP/s
+// (tensor pipe 54% active, exponentials 57%: the hand-off from products to
+// exponentials and back bounds it, each stream filling the other's gaps); 12
+// packed prompts of up to 1301 93 us; 509 tokens behind 3500 35 us; a token
+// each of 64 requests with up to 4096 keys 72 us, 5.0 TB/s; 16 + 2 heads, a token
+// after 30000 18 us; a prompt of 37 9 us.
+//
 // Every mbarrier wait is bounded (2 s); on expiry BL_ERR_TIMEOUT is recorded,
 // every role leaves its loop, copies and MMAs in flight drain, tensor memory
 // is freed and the CTA returns.
