@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from array import array
 from dataclasses import dataclass
@@ -210,11 +211,14 @@ def _call(fn, where: str, device: torch.device, *args):
     """fn(*args, stream) on the tensors' GPU and its current stream.  Entering a
     device costs more host time than the rest of a short call, so it is done
     only where another one is current."""
-    if _elsewhere(device):
+    index = device.index
+    if index is None or device.type != "cuda":
+        status = fn(*args, _stream(device))
+    elif index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             status = fn(*args, _stream(device))
     else:
-        status = fn(*args, _stream(device))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != BL_OK:
         raise BitLinearError(status, where)
 
@@ -679,16 +683,23 @@ def position_advance(pos: torch.Tensor):
 BL_FLAG_ROPE_HALVES = 8
 
 
-def _scratch(size, where: str, device: torch.device, *args) -> torch.Tensor:
-    """Device memory of the bytes that the library's `size` function says."""
+@functools.lru_cache(maxsize=1024)
+def _scratch_bytes(size: str, device: torch.device, *args) -> int:
+    """What the library's function `size` says on a device: it depends on the
+    arguments and the kind of GPU alone."""
     if _elsewhere(device):
         with torch.cuda.device(device):
-            n = size(*args)
+            n = getattr(_lib, size)(*args)
     else:
-        n = size(*args)
+        n = getattr(_lib, size)(*args)
     if not n:
-        raise BitLinearError(BL_ERR_SHAPE, where)
-    return torch.empty(n, dtype=torch.uint8, device=device)
+        raise BitLinearError(BL_ERR_SHAPE, size)
+    return n
+
+
+def _scratch(size: str, device: torch.device, *args) -> torch.Tensor:
+    """Device memory of the bytes that the library's function `size` says."""
+    return torch.empty(_scratch_bytes(size, device, *args), dtype=torch.uint8, device=device)
 
 
 def _heads(t, where: str, name: str, dtypes, heads, rows):
@@ -698,16 +709,16 @@ def _heads(t, where: str, name: str, dtypes, heads, rows):
         n, h, d = t.shape
         row, head, one = t.stride()
     except ValueError:
-        d = 0
+        n = h = d = row = head = one = 0
+    if d == 128 and one == 1 and (heads is None or h == heads) and (rows is None or n == rows) and t.dtype in dtypes:
+        return t.data_ptr(), n, row, head
     if t.dtype not in dtypes:
         want = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise BitLinearError(BL_ERR_DTYPE, where,
                              f"{name} is {str(t.dtype).replace('torch.', '')}, needs {want}")
-    if d != 128 or one != 1 or (heads is not None and h != heads) or (rows is not None and n != rows):
-        raise BitLinearError(
-            BL_ERR_SHAPE, where, f"{name} of shape {tuple(t.shape)} and strides {t.stride()} is not "
-            f"[{'rows' if rows is None else rows}][{'heads' if heads is None else heads}][128]")
-    return t.data_ptr(), n, row, head
+    raise BitLinearError(
+        BL_ERR_SHAPE, where, f"{name} of shape {tuple(t.shape)} and strides {t.stride()} is not "
+        f"[{'rows' if rows is None else rows}][{'heads' if heads is None else heads}][128]")
 
 
 _NO_HEADS = (0, 0, 0, 0)
@@ -785,8 +796,7 @@ def qk_norm_rope(q, k, v, positions, table, q_gain=None, k_gain=None, eps: float
 def attention_prefill_workspace(H: int, Hkv: int, device) -> torch.Tensor:
     """A workspace for attention_prefill of any lengths (reusable by ordered
     calls; its contents do not matter)."""
-    return _scratch(_lib.bitlinear_attention_prefill_workspace_bytes, "bitlinear_attention_prefill_workspace_bytes",
-                    torch.device(device), H, Hkv)
+    return _scratch("bitlinear_attention_prefill_workspace_bytes", torch.device(device), H, Hkv)
 
 
 def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=None,
@@ -836,8 +846,7 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=
 def adapter_workspace(T: int, r: int, device) -> torch.Tensor:
     """A workspace for adapter_add of up to T tokens and rank r (reusable by
     ordered calls; its contents do not matter)."""
-    return _scratch(_lib.bitlinear_adapter_workspace_bytes, "bitlinear_adapter_workspace_bytes",
-                    torch.device(device), T, r)
+    return _scratch("bitlinear_adapter_workspace_bytes", torch.device(device), T, r)
 
 
 def _rows(t, where: str, name: str, dtypes, rows: int, cols: int) -> int:
@@ -863,16 +872,17 @@ def adapter_add(y, x, down, up, index, scale=None, out=None, workspace=None):
     (the default is a new tensor).
     """
     where = "bitlinear_adapter_add"
-    if y.dim() != 2 or x.dim() != 2 or down.dim() != 3 or up.dim() != 3:
+    ys, xs, ds = y.shape, x.shape, down.shape
+    if len(ys) != 2 or len(xs) != 2 or len(ds) != 3 or up.dim() != 3:
         raise BitLinearError(BL_ERR_SHAPE, where, "y and x have two dimensions, down and up three")
-    (T, N), K, (n, r, dk) = y.shape, x.shape[1], down.shape
-    if dk != K or tuple(up.shape) != (n, N, r):
+    (T, N), K, (n, r, dk) = ys, xs[1], ds
+    if dk != K or up.shape != (n, N, r):
         raise BitLinearError(BL_ERR_SHAPE, where, f"down of shape {tuple(down.shape)} and up of shape "
                              f"{tuple(up.shape)} for K={K}, N={N}")
     device = y.device
     if out is None:
-        out = torch.empty(T, N, dtype=y.dtype, device=device)
-    if out.dtype != y.dtype:
+        out = torch.empty_like(y)
+    elif out.dtype != y.dtype:
         raise BitLinearError(BL_ERR_DTYPE, where, "out and y of different element types")
     ldy, ldx = _rows(y, where, "y", _FLOATS, T, N), _rows(x, where, "x", _BF16, T, K)
     ldo = _rows(out, where, "out", _FLOATS, T, N)
