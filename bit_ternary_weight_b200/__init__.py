@@ -811,7 +811,7 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=
     query i sees the keys 0 .. i + nk - nq, and gets zeros if there are none.
     So cu_q = cu_k is a batch of whole prompts, nk > nq a piece of a prompt
     behind a cached past, nq = 1 one new token for each request.  Rows of `out`
-    outside every sequence stay as they were.
+    outside every sequence stay as they were; out is none of q, k and v.
     """
     where = "bitlinear_attention_prefill"
     dims, kdims = q.shape, k.shape

@@ -756,6 +756,9 @@ int bitlinear_attention_prefill(const bitlinear_heads *q, const bitlinear_heads 
         !aligned_heads(*out, H, 2) || !aligned16(ws) || (reinterpret_cast<uintptr_t>(cu_q) & 3u) ||
         (reinterpret_cast<uintptr_t>(cu_k) & 3u))
         return BL_ERR_ALIGN;
+    // not in place: a tile's rows are read by every CTA that has a part of it
+    if (out->data == q->data || out->data == k->data || out->data == v->data)
+        return BL_ERR_SHAPE;
     const DeviceInfo *di;
     int st = need_device(&di);
     if (st)

@@ -683,11 +683,11 @@ typedef struct {
  *                value are written nowhere.  Non-negative slots are distinct.
  *   q_out        T rows of H heads, bf16;  k_out, v_out: rows of Hkv heads, bf16
  * The rows of an output do not overlap one another.  An output may be its
- * input itself (same place, element type and strides; no slots); any other
- * overlap leaves the overlapping values unspecified.  Rows that no slot names are left as they were.  A
- * position outside the table or a slot outside k_out records BL_ERR_SHAPE in
- * the device status word, and nothing is written for that token (position) or
- * for its key and value (slot).
+ * input itself (same place, element type and strides; keys and values only
+ * without slots); any other overlap leaves the overlapping values unspecified.
+ * Rows that no slot names are left as they were.  A position outside the table
+ * or a slot outside k_out records BL_ERR_SHAPE in the device status word, and
+ * nothing is written for that token (position) or for its key and value (slot).
  * 1 <= T < 2^31, H, Hkv <= 1024, D == 128.  flags: 0 or BL_FLAG_ROPE_HALVES.
  */
 int bitlinear_qk_norm_rope(const bitlinear_heads *q, const bitlinear_heads *k, const bitlinear_heads *v,
@@ -719,7 +719,8 @@ size_t bitlinear_attention_prefill_workspace_bytes(int H, int Hkv);
  * outside a sequence's rows, or behind the keys a query sees, has no effect on
  * that query, NaN and infinities included.  A query that sees a NaN or an
  * infinity of k or v has an unspecified output.
- *   q, out       rows of H heads, bf16 (out's rows do not overlap one another, nor q, k or v)
+ *   q, out       rows of H heads, bf16 (out's rows do not overlap one another, nor q, k or
+ *                v; out at the place of one of these is refused)
  *   k, v         rows of Hkv heads, bf16, with the same number of rows; H a multiple of
  *                Hkv, H / Hkv <= 64; D == 128
  *   cu_q, cu_k   device int32 [batch + 1], ascending, within the rows of q and k.

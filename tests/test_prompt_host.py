@@ -188,6 +188,11 @@ def test_attention_argument_errors_before_any_cuda_call(bl):
     for kw in (dict(q=_h(bl, data=A + 2)), dict(k=_h(bl, row=260)), dict(out=_h(bl, head=130, row=512)), dict(cu=A + 2),
                dict(ws=A + 8)):
         assert call(**kw) == bl.BL_ERR_ALIGN, kw
+    # not in place
+    for name in "qkv":
+        apart = {x: _h(bl, data=A + 4096 * i) for i, x in enumerate(("q", "k", "v", "out"))}
+        assert call(**{**apart, "out": apart[name]}) == bl.BL_ERR_SHAPE, name
+        assert call(**apart) not in (bl.BL_OK, bl.BL_ERR_NULL, bl.BL_ERR_SHAPE, bl.BL_ERR_ALIGN)   # no such memory
     assert L.bitlinear_attention_prefill_workspace_bytes(3, 2) == 0
     assert L.bitlinear_attention_prefill_workspace_bytes(65, 1) == 0
 
