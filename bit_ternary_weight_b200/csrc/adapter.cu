@@ -122,10 +122,14 @@ __global__ void __launch_bounds__(kChunk) adapter_order_kernel(const AdapterPara
     const int id = t < p.T ? token_id(p, t, true) : -1, bin = id < 0 ? kBins - 1 : id % (kBins - 1);
     const unsigned peers = __match_any_sync(0xffffffffu, bin);
     const int rank = __popc(peers & ((1u << lane) - 1));
-    // more than four adapters in the warp's two tiles
-    const bool mixed = __popc(__ballot_sync(0xffffffffu, id >= 0 && rank == 0)) > 4;
+    // the products that the chunk's tiles take as they come: worth an order above
+    // three for two tiles (2 adapters, alternating: 40 -> 28 us; prompts, which
+    // an order would only move: 27 -> 31)
+    const unsigned half = lane < kTile ? 0x0000ffffu : 0xffff0000u;
+    const int products = __syncthreads_count(id >= 0 && !(peers & half & ((1u << lane) - 1)));
+    const int tiles = int(min(int64_t(kChunk), p.T - c0) + kTile - 1) / kTile;
     int place = tid;
-    if (__syncthreads_or(mixed)) {
+    if (2 * products > 3 * tiles) {
         if (rank == 0)
             count[warp][bin] = uint16_t(__popc(peers));
         __syncthreads();
