@@ -844,8 +844,8 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, scale: float | None = None, out=
 
 
 def adapter_workspace(T: int, r: int, device) -> torch.Tensor:
-    """A workspace for adapter_add of up to T tokens and rank r (reusable by
-    ordered calls; its contents do not matter)."""
+    """A workspace for adapter_add of up to T tokens and ranks up to r (reusable
+    by ordered calls; its contents do not matter)."""
     return _scratch("bitlinear_adapter_workspace_bytes", torch.device(device), T, r)
 
 

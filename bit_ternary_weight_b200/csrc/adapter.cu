@@ -639,9 +639,13 @@ auto up_kernel(int r, Up kind, bool vec) -> void (*)(AdapterParams)
 size_t adapter_workspace_bytes(int64_t T, int r)
 {
     const DeviceInfo *di = device_info();
-    return di ? size_t(max_splits(T, di->sm_count)) * size_t(T) * size_t(r) * sizeof(float) +
-                    (T > kOrderTokens ? size_t(T) * sizeof(int2) : 0)
-              : 0;
+    if (!di)
+        return 0;
+    // A bound of max_splits(t) * t for every t up to T, since a workspace also
+    // serves fewer tokens, which may be split further: tiles times splits stay
+    // at 8 per SM or below unless every tile has one split.
+    const int64_t rows = std::max(T, std::min(32 * T, int64_t(8) * di->sm_count * kTile));
+    return size_t(rows) * size_t(r) * sizeof(float) + (T > kOrderTokens ? size_t(T) * sizeof(int2) : 0);
 }
 
 int launch_adapter_add(const AdapterArgs &a, cudaStream_t s)

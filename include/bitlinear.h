@@ -738,8 +738,9 @@ int bitlinear_attention_prefill(const bitlinear_heads *q, const bitlinear_heads 
                                 float scale, const bitlinear_heads *out, void *ws,
                                 size_t ws_bytes, unsigned flags, void *stream);
 
-/* Bytes of workspace bitlinear_adapter_add needs for T tokens and rank r on
- * the current device (0 if out of range). */
+/* Bytes of workspace that serve bitlinear_adapter_add for up to T tokens and
+ * ranks up to r on the current device: the size falls with neither (0 if out
+ * of range). */
 size_t bitlinear_adapter_workspace_bytes(int64_t T, int r);
 
 /*
@@ -756,7 +757,8 @@ size_t bitlinear_adapter_workspace_bytes(int64_t T, int r);
  *   index        device int32 [T], below n.  An index at or above n records
  *                BL_ERR_SHAPE in the device status word; that token's out is y.
  *   scale        NULL (1) or device fp32 [n]
- *   ws           device workspace of at least bitlinear_adapter_workspace_bytes;
+ *   ws           device workspace, 16-byte aligned, of at least
+ *                bitlinear_adapter_workspace_bytes (of these or of larger T and r);
  *                contents on entry are ignored.  Not shared by calls that can
  *                run at the same time.
  * Both products run on the tensor cores on bf16 operands with fp32
