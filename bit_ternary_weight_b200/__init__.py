@@ -684,9 +684,7 @@ BL_FLAG_ROPE_HALVES = 8
 
 
 @functools.lru_cache(maxsize=1024)
-def _scratch_bytes(size: str, device: torch.device, *args) -> int:
-    """What the library's function `size` says on a device: it depends on the
-    arguments and the kind of GPU alone."""
+def _scratch_bytes_on(size: str, device: torch.device, *args) -> int:
     if _elsewhere(device):
         with torch.cuda.device(device):
             n = getattr(_lib, size)(*args)
@@ -695,6 +693,15 @@ def _scratch_bytes(size: str, device: torch.device, *args) -> int:
     if not n:
         raise BitLinearError(BL_ERR_SHAPE, size)
     return n
+
+
+def _scratch_bytes(size: str, device: torch.device, *args) -> int:
+    """What the library's function `size` says on a device: it depends on the
+    arguments and the GPU alone, and is remembered for these.  A device without
+    an index is the current one, which may be another at the next call."""
+    if device.index is None and device.type == "cuda":
+        device = torch.device("cuda", torch.cuda.current_device())
+    return _scratch_bytes_on(size, device, *args)
 
 
 def _scratch(size: str, device: torch.device, *args) -> torch.Tensor:
