@@ -320,6 +320,13 @@ struct Cols {
             }
         }
     }
+    // The elements as they were loaded.
+    __device__ __forceinline__ void copy(char *dst) const
+    {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i)
+            reinterpret_cast<uint4 *>(dst)[i] = v[i];
+    }
     static __device__ __forceinline__ void store(char *dst, const float (&f)[8])
     {
         if constexpr (F32) {
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
                     continue;
                 }
             }
-            // out = y + the product with adapter a (-1: y) for some of the tile's rows
+            // out = y + the product with adapter a for some of the tile's rows
             auto finish = [&](unsigned rows, int a) {
                 float acc[4][4] = {};
                 if constexpr (VEC) {
@@ -524,8 +531,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
                                 acc[e / 2][2 * h + e % 2] = f[h][e];
                         }
                     }
-                    if (a >= 0)
-                        product(a, acc);
+                    product(a, acc);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if ((rows >> (g + 8 * h) & 1) && own) {
@@ -538,8 +544,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
                 } else {
                     const int64_t n = n0 + lane;
                     rows = n < p.N ? rows : 0;
-                    if (a >= 0)
-                        product(a, acc);
+                    product(a, acc);
                     __syncwarp();                             // the last sums have been read
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -554,10 +559,32 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
                                     __uint_as_float(w[r]) + reinterpret_cast<const float *>(sums[warp][r])[lane]);
                 }
             };
+            // out = y, bit for bit (a sum with zero would lose the sign of -0)
+            auto keep = [&](unsigned rows) {
+                if constexpr (VEC) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if ((rows >> (g + 8 * h) & 1) && own)
+                            y[i][h].copy(dst(h));
+                } else {
+                    const int64_t n = n0 + lane;
+                    rows = n < p.N ? rows : 0;
+#pragma unroll
+                    for (int r = 0; r < kTile; ++r) {
+                        if (rows >> r & 1) {
+                            char *at = op + (token_s[r] * p.ldo + n) * kElem;
+                            if constexpr (F32)
+                                *reinterpret_cast<uint32_t *>(at) = w[r];
+                            else
+                                *reinterpret_cast<uint16_t *>(at) = uint16_t(w[r] >> 16);
+                        }
+                    }
+                }
+            };
             unsigned firsts = first_of(id, lane);
             const unsigned none = __ballot_sync(0xffffffffu, lane < valid && id < 0);
             if (way == 0 && none)
-                finish(none, -1);
+                keep(none);
             for (int ord = 0; firsts; ++ord, firsts &= firsts - 1) {
                 if (WAYS > 1 && ord % WAYS != way)
                     continue;

@@ -746,7 +746,7 @@ size_t bitlinear_adapter_workspace_bytes(int64_t T, int r);
 /*
  * Low-rank adapters of many requests beside one shared projection:
  *   out[t] = y[t] + scale[a] * up[a] (down[a] x[t]),  a = index[t]
- * and out[t] = y[t] where index[t] < 0 (no adapter).  Tokens of different
+ * and out[t] = y[t], bit for bit, where index[t] < 0 (no adapter).  Tokens of different
  * adapters may come in any order.  The pages have no counterpart: packed
  * ternary weights are shared and frozen, an adapter is how one request's
  * model differs from another's.
