@@ -339,15 +339,30 @@ struct Cols {
     }
 };
 
+// a's first bf16 term, and a without it: an infinity or a NaN is its own first
+// term and leaves nothing (not inf - inf), and a finite value that would round
+// to infinity takes the largest finite bf16 and the rest.
+__device__ __forceinline__ float first_term(float a, float &rest)
+{
+    constexpr float kMax = 3.38953139e38f;                    // 0x7f7f0000
+    const bool finite = fabsf(a) <= 3.40282347e38f;
+    const float t = __bfloat162float(__float2bfloat16_rn(finite ? fminf(fmaxf(a, -kMax), kMax) : a));
+    rest = finite ? a - t : 0.0f;
+    return t;
+}
+
 // The values (a, b) as sums of TERMS bf16 values, largest first.
 template <int TERMS>
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[TERMS])
 {
+    float ra, rb;
+    const float ta = first_term(a, ra), tb = first_term(b, rb);
+    w[0] = pack_bf16(ta, tb);
 #pragma unroll
-    for (int i = 0; i < TERMS; ++i) {
-        w[i] = pack_bf16(a, b);
-        a -= __uint_as_float(w[i] << 16);
-        b -= __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 1; i < TERMS; ++i) {
+        w[i] = pack_bf16(ra, rb);
+        ra -= __uint_as_float(w[i] << 16);
+        rb -= __uint_as_float(w[i] & 0xffff0000u);
     }
 }
 

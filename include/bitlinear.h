@@ -764,7 +764,9 @@ size_t bitlinear_adapter_workspace_bytes(int64_t T, int r);
  * Both products run on the tensor cores on bf16 operands with fp32
  * accumulators; the r values between them enter the second as a sum of bf16
  * values (two, 16 bits of mantissa, for bf16 outputs, three for fp32 outputs).
- * Sums have a fixed order: the same call gives the same bits.
+ * Sums have a fixed order: the same call gives the same bits.  One of the r
+ * values that passes fp32's range is infinite, as in the formula; NaN and infinity in x, down
+ * or up reach only the tokens that use them, whose outputs are then unspecified.
  * r a multiple of 8, 8 <= r <= 128; K % 64 == 0; x, down and up 16-byte
  * aligned, ldx such that rows are.  1 <= T < 2^31, 1 <= n <= 65536.  flags: 0.
  */
