@@ -6,9 +6,10 @@
 // keys before attention).  Per head x of 128 values (all in fp32):
 //   r = 1 / sqrt(mean x^2 + eps),  h = (x * r) * g      (only with a gain)
 //   (a, b) <- (a c - b s, a s + b c)                     (c, s) of the position
-// rounded once to bf16.  The rotation's operations and their order are those
-// of attention.cu, so a prompt's cache rows equal the rows that its tokens
-// would get one at a time.
+// rounded once to bf16.  Without a gain the rotation's operations and their
+// order are those of attention.cu, so a prompt's cache rows equal the rows that
+// its tokens would get one at a time; with one, gains are folded into the
+// angles and r is applied last (below).
 //
 // Memory-bound: every element is read once and written once, so the design is
 // about bytes in flight.  A warp takes the heads of a token (or a part of

@@ -669,9 +669,14 @@ typedef struct {
  * for one token.
  *   r   = 1 / sqrt(mean_d x[d]^2 + eps)  (the sum in fp32), x <- (x r) g[d]
  *   (a, b) <- (a c - b s, a s + b c),  (c, s) = table[position][i] for the
- *         pair (2i, 2i + 1), or (i, i + 64) with BL_FLAG_ROPE_HALVES; the
- *         products and sums in fp32 in that order, rounded once to bf16.
- * Without gains this is bit for bit the rotation of bitlinear_attention_decode.
+ *         pair (2i, 2i + 1), or (i, i + 64) with BL_FLAG_ROPE_HALVES; in fp32,
+ *         rounded once to bf16.
+ * Heads without a gain: the products and sums in that order, each rounded, bit
+ * for bit the rotation of bitlinear_attention_decode.  Heads with a gain: the
+ * gain goes into the angles first and r comes last,
+ *   (r (a (g_a c) - b (g_b s)), r (a (g_a s) + b (g_b c)))
+ * with fused multiply-adds, so the last fp32 bits (and now and then the bf16
+ * one) are not those of the order above.
  *   q, k, v      T rows of H, Hkv, Hkv heads, dtype xt (BL_BF16 or BL_F32); v may
  *                be NULL together with v_out (keys and queries only)
  *   positions    device int32 [T]
