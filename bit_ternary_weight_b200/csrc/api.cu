@@ -747,8 +747,9 @@ int bitlinear_attention_prefill(const bitlinear_heads *q, const bitlinear_heads 
 {
     if (!q || !k || !v || !out || !cu_q || !cu_k || !q->data || !k->data || !v->data || !out->data)
         return BL_ERR_NULL;
+    // the exponentials are to base 2: scale * log2(e) has to be finite too
     if (D != 128 || !valid_groups(H, Hkv) || batch < 1 || batch > 65535 || !(scale > 0.0f) ||
-        !(scale <= 3.0e38f) || flags || !valid_heads(*q, H) || !valid_heads(*k, Hkv) ||
+        !(scale <= 2.35e38f) || flags || !valid_heads(*q, H) || !valid_heads(*k, Hkv) ||
         !valid_heads(*v, Hkv) || !valid_heads(*out, H) || v->rows != k->rows || out->rows != q->rows ||
         !distinct_heads(*out, H))
         return BL_ERR_SHAPE;

@@ -731,7 +731,8 @@ size_t bitlinear_attention_prefill_workspace_bytes(int H, int Hkv);
  *   cu_q, cu_k   device int32 [batch + 1], ascending, within the rows of q and k.
  *                A sequence whose bounds are not records BL_ERR_SHAPE in the
  *                device status word and writes nothing.
- *   scale        > 0; 1 / sqrt(128) is usual
+ *   scale        > 0, up to 2.35e38 (what it is in base 2 is finite too);
+ *                1 / sqrt(128) is usual
  *   ws, ws_bytes device workspace, 16-byte aligned, of at least
  *                bitlinear_attention_prefill_workspace_bytes; its contents on
  *                entry are ignored.  Not shared by calls that can run at the same time.
