@@ -29,9 +29,10 @@ from dataclasses import dataclass, field
 
 import torch
 
-from . import (BL_ACT_PLAIN, BL_ACT_RELU2_GATE, BL_ACT_RMSNORM, BL_ERR_SHAPE, BitLinearError,
-               attention_decode, attention_prefill, attention_workspace, decode_linear, gemm, pack,
-               position_advance, qk_norm_rope, quantize_act, rmsnorm_quantize_act, rope_table)
+from . import (BL_ACT_PLAIN, BL_ACT_RELU2_GATE, BL_ACT_RMSNORM, BL_ERR_DTYPE, BL_ERR_SHAPE,
+               BitLinearError, attention_decode, attention_prefill, attention_workspace,
+               decode_linear, gemm, pack, position_advance, qk_norm_rope, quantize_act,
+               rmsnorm_quantize_act, rope_table)
 
 
 @dataclass
@@ -166,10 +167,13 @@ class Decoder:
         fp64).  The gate and the residual sums between the kernels are plain
         fp32 torch operations."""
         c = self.cfg
-        T = x.shape[0]
-        if x.dim() != 2 or x.shape[1] != c.hidden or T < 1 or start < 0 or start + T > c.max_seq:
+        T = x.shape[0] if x.dim() == 2 else 0
+        if T < 1 or x.shape[1] != c.hidden or start < 0 or start + T > c.max_seq:
             raise BitLinearError(BL_ERR_SHAPE, "Decoder.prefill",
                                  f"x of shape {tuple(x.shape)} at position {start} of {c.max_seq}")
+        if x.dtype != torch.bfloat16:
+            raise BitLinearError(BL_ERR_DTYPE, "Decoder.prefill",
+                                 f"x is {str(x.dtype).replace('torch.', '')}, needs bfloat16")
         D, dev = c.head_dim, x.device
         positions = torch.arange(start, start + T, dtype=torch.int32, device=dev)
         # [0, n] without a copy from the host
