@@ -26,9 +26,13 @@
 // one before: two (16 bits of it) for bf16 outputs, three (24 bits) for fp32
 // outputs; one alone would cost an output 2^-8 of the adapter's share.
 // Measured (inputs that change from call to call): 4093 tokens of prompts, 2560
-// to 6912 columns, rank 16, 136 MB: 44 us, 3.1 TB/s, of which the order takes 1,
-// the first product 15 and the second 28; 32 tokens of 24 adapters, 2560 x 2560:
-// 11 us, a token at rank 64: 8 us, three to four memory latencies in a row each.
+// to 6912 columns, rank 16, 136 MB: 44.7 us, 3.0 TB/s, of which the order takes 1,
+// the first product 15 and the second 28; at rank 64 91 us.  32 tokens of 24
+// adapters, 2560 x 2560: 10.7 us, a token at rank 64 (fp32): 7.6 us, three to four
+// memory latencies in a row each.  Ranks above 64 are the ones without room: the
+// second product's kernels hold 64 registers of `up` a lane and spill up to 168
+// bytes at 128 registers, and take a tile at a time: 170 us at rank 72, 204 at
+// 128 for the prompts; 18 and 21 us for the 32 tokens.
 #include <algorithm>
 
 #include "bl_common.cuh"
@@ -372,13 +376,15 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[TERMS
 // they share 32 columns and the adapters of one tile.  y and the adapters are
 // asked for while the first launch still runs.  u, the K splits' parts added
 // in order, is split into its bf16 terms once per CTA, and the operand of the
-// last adapter stays from tile to tile (prompts).  The accumulators start at y
-// (bf16 outputs; an fp32 output adds y at the end, since a tensor core's sums
-// lose up to 2^-23 of y each), whichever tokens share the tile, so that a token
-// gets the same bits beside any others where the K splits are the same.  Rows that
-// are not whole 16-byte vectors (VEC = false) go through shared memory, so
-// that a warp reads and writes 32 columns of a row at once: 4096 tokens, 704 x
-// 1001, rank 16, 26 us instead of 35 with a lane's eight columns one by one.
+// last adapter stays from tile to tile (prompts).  For bf16 rows of whole
+// 16-byte vectors the accumulators start at y; fp32 rows (a tensor core's sums
+// would lose up to 2^-23 of y each) and rows that are not whole vectors add y at
+// the end.  Which of the two goes by the row layout and the type, whichever tokens
+// share the tile, so that a token gets the same bits beside any others where the
+// K splits are the same.  Rows that are not whole vectors (VEC = false) go through
+// shared memory, so that a warp reads and writes 32 columns of a row at once:
+// 4096 tokens, 704 x 1001, rank 16, 26 us instead of 35 with a lane's eight
+// columns one by one.
 template <int KB, bool F32, int WAYS, int TILES, bool VEC>
 __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const AdapterParams p)
 {
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) adapter_up_kernel(const Adap
 }
 
 // Tiles of a run: as many as leave the adapter's operand (8 KB registers) and
-// the tiles' y in registers.
+// the tiles' y in registers up to KB = 4; at KB = 8 one tile already spills.
 constexpr int run_tiles(int kb, bool f32) { return kb > 4 ? 1 : kb > 2 ? (f32 ? 1 : 2) : f32 ? 2 : 4; }
 
 // With fewer tokens, the adapters of a tile have warps and CTAs of their own.

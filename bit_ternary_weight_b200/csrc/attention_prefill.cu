@@ -44,12 +44,14 @@
 //                   product (a zero weight times a NaN would reach rows that
 //                   do not see it) and rows that do see them get NaN.
 //
-// Measured (20 + 5 heads, with the join): a prompt of 8192 303 us, 1.13 PFLOP/s
-// (tensor pipe 54% active, exponentials 57%: the hand-off from products to
-// exponentials and back bounds it, each stream filling the other's gaps); 12
-// packed prompts of up to 1301 93 us; 509 tokens behind 3500 35 us; a token
-// each of 64 requests with up to 4096 keys 72 us, 5.0 TB/s; 16 + 2 heads, a token
-// after 30000 18 us; a prompt of 37 9 us.
+// Measured (20 + 5 heads, with the join; a graph of nine calls): a prompt of 8192
+// 296 to 303 us, 1.13 to 1.16 PFLOP/s (tensor pipe 54% active, exponentials 57%: the
+// hand-off from products to exponentials and back bounds it, each stream filling
+// the other's gaps); 12 packed prompts of up to 1301 93 us; 509 tokens behind 3500
+// 35 us; a token each of 64 requests with up to 4096 keys 71 us, 5.1 TB/s; 16 + 2
+// heads, a token after 30000 18 us; a prompt of 37 8.7 us.  Repeated for seconds, at
+// the clocks that the power limit leaves: 347 us, 0.99 PFLOP/s, for the prompt of
+// 8192 and 77 to 81 us, 4.5 to 4.7 TB/s, for the 64 requests.
 //
 // Every mbarrier wait is bounded (2 s); on expiry BL_ERR_TIMEOUT is recorded,
 // every role leaves its loop, copies and MMAs in flight drain, tensor memory
