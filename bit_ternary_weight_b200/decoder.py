@@ -178,7 +178,7 @@ class Decoder:
         positions = torch.arange(start, start + T, dtype=torch.int32, device=dev)
         # [0, n] without a copy from the host
         cu_q, cu_k = (torch.arange(0, 2 * n, n, dtype=torch.int32, device=dev) for n in (T, start + T))
-        h = x
+        h = x.detach()      # no gradients: self.h would keep the graph of x
         for L in self.layers:
             act = rmsnorm_quantize_act(h, L.g_attn, c.eps)
             q, k, v = (gemm(w, *act).view(T, -1, D) for w in (L.q, L.k, L.v))

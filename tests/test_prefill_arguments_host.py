@@ -32,3 +32,11 @@ def test_a_prompt_up_to_the_last_row():
     d, x = _decoder(), torch.arange(4 * 64).view(4, 64).to(BF16)
     assert torch.equal(d.prefill(x, 4), x)
     assert d.pos.item() == 8 and torch.equal(d.h, x[-1])
+
+
+def test_streams_that_require_gradients_leave_no_graph_behind():
+    """An embedding's output, for example: nothing of its graph is kept."""
+    d, x = _decoder(), torch.ones(4, 64, dtype=BF16).requires_grad_()
+    y = d.prefill(x * 2)
+    assert not y.requires_grad and not d.h.requires_grad and d.h.grad_fn is None
+    assert torch.equal(d.h, torch.full((64,), 2.0, dtype=BF16))
