@@ -76,7 +76,10 @@ constexpr uint32_t kTile = 2 * kBox;      // 128 x 128 bf16
 constexpr int kItems = 4;                 // work list ring
 constexpr int kTileExtra = 2;             // what a tile costs besides its key blocks, in key blocks
 constexpr float kRescale = 8.0f;          // log2 of the growth of a row's weights before O is rescaled
-// Registers: 168 a thread at launch; a softmax thread holds its row of S.
+// Registers: 168 a thread at launch; a softmax thread holds its row of S.  They
+// leave no room on an SM for a CTA of the kernel before this one, so a kernel that
+// lets its dependents start before it allocates tensor memory (gemv_tc.cu) never
+// finds all of it taken here by a CTA that waits for that kernel's end.
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 

@@ -20,7 +20,7 @@
 // ahead, 39 us.  What bounds it is the arithmetic's latency at 12 warps an SM:
 // without any store it still takes 30 us.  (8 warps of three slots: 36 us.)
 // 1283 tokens in fp32 (30 MB): 8.3 us; a slot holds 16 fp32 heads, so a token is
-// two items, 2566 on 1776 warps, and most warps idle in the second round.
+// two items, 2566 on 1776 warps, and most warps have no second one.
 // Eight lanes take a head from the slot, each
 // with dimensions 8c .. 8c + 7 and 64 + 8c .. 64 + 8c + 7, so that every access
 // is 16 bytes a lane and both kinds of pairs ((2i, 2i + 1) and (i, i + 64)) are
